@@ -334,6 +334,105 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
                                            void *stream);
 
 /* --------------------------------------------------------------------------
+ * The 4-bit paged KV cache: the codes of bitnet_kv_quant's 4- and 3-bit rows, two to a
+ * byte, in pages that grow token by token.
+ * Definition: bitnet_v2_engine.py page, BitNetV2Attention._quantize_kv_head (the
+ * quantisers and the 8-bit BOS row) and BitNetV2Attention.forward (attention over the
+ * fake-quantised keys and values); packing and paging are this library's storage.
+ *
+ * bitnet_kv4_cache_t: six device arrays, owned by the caller (16-byte aligned).
+ *   k_codes, v_codes  uint8 [pages][heads][page_size][dim/2]: byte j of a row holds the
+ *                     code of dimension 2j in its low and of 2j+1 in its high four
+ *                     bits, two's complement.
+ *   k_step, v_step    fp32 [pages][heads][page_size]: value = step * code.
+ *   k_bos, v_bos      int8 [pages][heads][dim]: the 8-bit codes of position 0 of the
+ *                     sequence whose first page this is (its step is in k_step and
+ *                     v_step, row 0; its 4-bit row is not read).
+ *   page_size is 16, 32, 64, 128 or 256; dim is 64, 128 or 256; heads is the number of
+ *   key heads (BITNET_ERR_UNSUPPORTED_SHAPE otherwise).
+ *   Nothing needs initialising: rows that no write has reached are never read.
+ *
+ * bitnet_kv4_batch_t: the batch a call works on, device arrays of int32.
+ *   q_starts     [batch + 1], not decreasing, q_starts[0] >= 0: sequence b owns rows
+ *                q_starts[b] .. q_starts[b+1] - 1 of the call's token tensors.  Rows before
+ *                q_starts[0] and from q_starts[batch] on belong to no sequence; outputs
+ *                there are left as they are.
+ *   kv_lens      [batch]: positions in the cache once this step's rows are written.
+ *                The n_b rows of sequence b stand at positions kv_lens[b] - n_b ..
+ *                kv_lens[b] - 1.
+ *   block_table  [batch][table_stride], of which the first max_pages of a row are
+ *                used: position s is row s % page_size of page block_table[b][s / page_size].
+ *                Entries that no position in use needs may hold anything (-1, say).
+ *   A page number outside [0, pages), or a length past max_pages * page_size, where a
+ *   position needs it, records BITNET_ERR_INVALID_ARG in the device status word; that
+ *   position is then not written, reads as zeros, and is not attended.  Sequences of a
+ *   batch may share pages for reading; rows written by one call must lie in different
+ *   places.
+ *
+ * bitnet_kv4_write: quantises new rows and writes them to their positions.
+ *   Row x of position s, in real arithmetic (decided in fp64 wherever fp32 is near a border,
+ *   so codes do not depend on an order of summation):
+ *     s = 0:            stat = max|x|,  Q = 127,    codes in [-128, 127]  (k_bos / v_bos)
+ *     s >= 1, bits = 4: stat = mean|x|, Q = sqrt 7, codes in [-8, 7]
+ *     s >= 1, bits = 3: stat = max|x|,  Q = 3,      codes in [-4, 3]
+ *     code = clamp(rne(x * (Q / (stat + eps)))),  step = (stat + eps) / Q.
+ *   k, v     [T][heads][dim] fp32 or bf16 (dt); element (t, h, d) of either at
+ *            t * token_stride + h * head_stride + d (elements; row starts must be 16-byte aligned).
+ *   Rows whose position would be negative (n_b > kv_lens[b]) are skipped.
+ *
+ * bitnet_kv4_read: the rows at the same positions, as values.
+ *   k_out, v_out  [T][heads][dim], fp32, or bf16 (the fp32 value rounded to nearest
+ *                 even); either may be NULL.  With n_b = kv_lens[b] it reads a whole sequence.
+ *                 Rows of negative positions are written as zeros.
+ *
+ * bitnet_kv4_attention: softmax attention of the batch's rows over the cache.
+ *   Query row i of sequence b stands at p = kv_lens[b] - n_b + i; query head h reads key
+ *   head h / (q_heads / heads).  With the values of the cached positions t in
+ *     [0, kv_lens[b])                    causal = 0
+ *     [max(0, p - window + 1), p]        causal = 1 (window = 0: from 0)
+ *     s_t = scale * q . k_t;  out = sum_t e^(s_t) v_t / sum_t e^(s_t);  lse = log sum_t e^(s_t).
+ *   A row that sees no position gives out = 0 and lse = -infinity.
+ *   q        [T][q_heads][dim] fp32 or bf16 (dt), strides as above.
+ *   out      [T][q_heads][dim] of dt, densely packed;  lse [T][q_heads] fp32 or NULL.
+ *   q_heads  a multiple of heads.  window >= 0, and 0 unless causal.
+ *   max_q    0, or the largest n_b of the batch where the caller knows it (a hint for
+ *            the choice of kernel; results stay right where it is wrong).
+ *   ws       device scratch of at least bitnet_kv4_attention_workspace_bytes(...) bytes
+ *            (256-byte aligned; BITNET_ERR_WORKSPACE if smaller).  Its contents need no
+ *            initialisation.
+ *   Products and sums are fp32 (codes and scaled queries enter the tensor cores exactly in bf16
+ *   calls; fp32 calls split queries and probabilities into two fp16 parts); sums run in a fixed
+ *   order, so equal calls give equal bits.  scale must be finite.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    uint8_t *k_codes, *v_codes;
+    float *k_step, *v_step;
+    int8_t *k_bos, *v_bos;
+    int64_t pages;
+    int32_t heads, page_size, dim;
+} bitnet_kv4_cache_t;
+
+typedef struct {
+    const int32_t *block_table, *kv_lens, *q_starts;
+    int64_t table_stride;
+    int32_t batch, max_pages;
+} bitnet_kv4_batch_t;
+
+BITNET_API bitnet_status_t bitnet_kv4_write(const void *k, const void *v, bitnet_dtype_t dt, int64_t T,
+                                            int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                            int64_t v_head_stride, const bitnet_kv4_cache_t *cache,
+                                            const bitnet_kv4_batch_t *batch, int bits, float eps, void *stream);
+BITNET_API bitnet_status_t bitnet_kv4_read(const bitnet_kv4_cache_t *cache, const bitnet_kv4_batch_t *batch, int64_t T,
+                                           void *k_out, void *v_out, bitnet_dtype_t dt, void *stream);
+BITNET_API size_t bitnet_kv4_attention_workspace_bytes(int64_t T, int64_t q_heads, int64_t heads, int64_t dim,
+                                                       int64_t batch);
+BITNET_API bitnet_status_t bitnet_kv4_attention(const void *q, bitnet_dtype_t dt, int64_t T, int64_t q_heads,
+                                                int64_t q_token_stride, int64_t q_head_stride,
+                                                const bitnet_kv4_cache_t *cache, const bitnet_kv4_batch_t *batch,
+                                                float scale, int causal, int64_t window, int64_t max_q, void *out,
+                                                float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* --------------------------------------------------------------------------
  * Prefill GEMM tile control (no counterpart on the pages).
  * bitnet_gemm_token_tile: the token-tile size (256, 224, 192, 128 or 64 tokens
  *   per tensor-core tile) that bitnet_ternary_gemm uses for an M x N x K problem

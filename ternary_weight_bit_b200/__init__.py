@@ -31,6 +31,7 @@ __all__ = [
     "bitnet_hbitlinear_forward_tl2",
     "bitnet_act_quant_swiglu", "bitnet_hbitlinear_forward_swiglu", "bitnet_kv_quant",
     "bitnet_ternary_gemm_ex", "bitnet_hbitlinear_forward_ex",
+    "KV4Cache", "bitnet_kv4_write", "bitnet_kv4_read", "bitnet_kv4_attention", "bitnet_kv4_attention_workspace_bytes",
 ]
 
 _MODES = {"int8": _native.ACT_INT8_ABSMAX, "int4": _native.ACT_INT4_ABSMEAN}
@@ -413,6 +414,168 @@ def bitnet_hbitlinear_forward_tl2(X: torch.Tensor, tl2: torch.Tensor, alpha: tor
                                                   mode_id(mode), _ptr(tl2), _ptr(alpha), N, _ptr(out), _ptr(ws),
                                                   ws.numel(), _stream(stream)))
     return out
+
+
+class KV4Cache:
+    """The 4-bit paged KV cache: six tensors on one CUDA device (layout in include/bitnet.h).
+
+    k_codes, v_codes uint8 [pages, heads, page_size, dim/2]; k_step, v_step fp32 [pages, heads, page_size];
+    k_bos, v_bos int8 [pages, heads, dim].  KV4Cache.empty allocates them (page 16, 32, 64, 128 or 256;
+    dim 64, 128 or 256).  The object keeps the tensors' addresses; a batch of sequences is described to the
+    calls by three int32 CUDA tensors:
+
+        block_table [B, max_pages]  page of position s of sequence b: block_table[b, s // page_size]
+        kv_lens     [B]             positions in the cache, this step's rows included
+        q_starts    [B + 1]         sequence b owns rows q_starts[b]:q_starts[b + 1] of the token tensors, at
+                                    its last positions
+
+    A step of a model writes its new keys and values, then attends:
+
+        bitnet_kv4_write(k, v, cache, block_table, kv_lens, q_starts)
+        out = bitnet_kv4_attention(q, cache, block_table, kv_lens, q_starts)
+    """
+
+    def __init__(self, k_codes, v_codes, k_step, v_step, k_bos, v_bos):
+        _need(k_codes, "k_codes", torch.uint8)
+        if k_codes.dim() != 4:
+            raise ValueError(f"k_codes must be [pages, heads, page_size, dim/2], got {tuple(k_codes.shape)}")
+        pages, heads, page, half = k_codes.shape
+        self.device = k_codes.device
+        self.pages, self.heads, self.page_size, self.dim = pages, heads, page, 2 * half
+        for name, t, dtype, shape in (("v_codes", v_codes, torch.uint8, (pages, heads, page, half)),
+                                      ("k_step", k_step, torch.float32, (pages, heads, page)),
+                                      ("v_step", v_step, torch.float32, (pages, heads, page)),
+                                      ("k_bos", k_bos, torch.int8, (pages, heads, self.dim)),
+                                      ("v_bos", v_bos, torch.int8, (pages, heads, self.dim))):
+            _need(t, name, dtype, shape)
+            if t.device != self.device:
+                raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        self.k_codes, self.v_codes, self.k_step, self.v_step = k_codes, v_codes, k_step, v_step
+        self.k_bos, self.v_bos = k_bos, v_bos
+        self._c = _native.Kv4Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_step.data_ptr(), v_step.data_ptr(),
+                                   k_bos.data_ptr(), v_bos.data_ptr(), pages, heads, page, self.dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, page_size: int = 64, device="cuda") -> "KV4Cache":
+        """A cache whose memory is not initialised (rows that no write has reached are never read)."""
+        if dim % 2:
+            raise ValueError(f"dim must be even, got {dim}")
+        codes = [torch.empty((pages, heads, page_size, dim // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+        steps = [torch.empty((pages, heads, page_size), dtype=torch.float32, device=device) for _ in range(2)]
+        bos = [torch.empty((pages, heads, dim), dtype=torch.int8, device=device) for _ in range(2)]
+        return cls(*codes, *steps, *bos)
+
+
+def _kv4_batch(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor):
+    if not isinstance(cache, KV4Cache):
+        raise TypeError("cache must be a KV4Cache")
+    B = kv_lens.shape[0] if isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1 else -1
+    _need(kv_lens, "kv_lens", torch.int32, (B,))
+    _need(q_starts, "q_starts", torch.int32, (B + 1,))
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
+    dev = cache.device
+    if block_table.device != dev or kv_lens.device != dev or q_starts.device != dev:
+        raise ValueError(f"block_table, kv_lens and q_starts must be on the cache's device {dev}")
+    width = block_table.shape[1]
+    return _native.Kv4Batch(block_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr(), width, B, width)
+
+
+def _rows(t: torch.Tensor, name: str, cache: KV4Cache, heads=None):
+    """Checks a [T, heads, dim] tensor whose rows of dim lie anywhere; returns (T, token stride, head stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != cache.device:
+        raise ValueError(f"{name} must be a CUDA tensor on the cache's device {cache.device}")
+    if t.dim() != 3 or t.shape[2] != cache.dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape [T, {'heads' if heads is None else heads}, {cache.dim}], "
+                         f"got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    # the stride of a dimension of one says nothing
+    return t.shape[0], t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def _kv4_call(cache: KV4Cache, fn: str, stream, *args) -> None:
+    """The call with the cache's device current (a kernel is launched on the current one)."""
+    f = getattr(_native.load(), fn)
+    if cache.device.index == torch.cuda.current_device():
+        _native.check(fn, f(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(cache.device):
+            _native.check(fn, f(*args, _stream(stream)))
+
+
+def bitnet_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor,
+                     kv_lens: torch.Tensor, q_starts: torch.Tensor, bits: int = 4, eps: float = 1e-5,
+                     stream=None) -> None:
+    """Quantise the new rows k, v [T, heads, dim] (fp32 or bf16, any token and head strides) into the cache, at
+    the last positions of their sequences.  Position 0 is kept at 8 bits, the others at `bits` (4: absmean,
+    3: absmax).  kv_lens counts the new rows."""
+    batch = _kv4_batch(cache, block_table, kv_lens, q_starts)
+    T, kts, khs = _rows(k, "k", cache, cache.heads)
+    Tv, vts, vhs = _rows(v, "v", cache, cache.heads)
+    if Tv != T or v.dtype != k.dtype:
+        raise ValueError(f"v must have {T} rows of {k.dtype}, got {Tv} of {v.dtype}")
+    _kv4_call(cache, "bitnet_kv4_write", stream, k.data_ptr(), v.data_ptr(), _xdt(k), T, kts, khs, vts, vhs,
+              cache._ref, ctypes.byref(batch), bits, eps)
+
+
+def bitnet_kv4_read(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor,
+                    total: int, dtype=torch.float32, k_out=None, v_out=None, stream=None):
+    """The cached values of the batch's rows (the last q_starts[b+1] - q_starts[b] positions of sequence b) as
+    (k, v), each [total, heads, dim] of dtype.  Rows that belong to no sequence are left as they are."""
+    batch = _kv4_batch(cache, block_table, kv_lens, q_starts)
+    dt = _out_dt(dtype)
+    shape = (total, cache.heads, cache.dim)
+    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _need(t, name, dtype, shape)
+        if t.device != cache.device:
+            raise ValueError(f"{name} must be on the cache's device {cache.device}")
+    _kv4_call(cache, "bitnet_kv4_read", stream, cache._ref, ctypes.byref(batch), total, k_out.data_ptr(),
+              v_out.data_ptr(), dt)
+    return k_out, v_out
+
+
+def bitnet_kv4_attention_workspace_bytes(T: int, q_heads: int, heads: int, dim: int, batch: int) -> int:
+    """Workspace of bitnet_kv4_attention for T rows of q_heads over a cache of `heads` key heads (0: sizes it refuses)."""
+    return _native.load().bitnet_kv4_attention_workspace_bytes(T, q_heads, heads, dim, batch)
+
+
+def bitnet_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                         q_starts: torch.Tensor, scale=None, causal: bool = True, window: int = 0, max_q: int = 0,
+                         return_lse: bool = False, out=None, lse=None, ws=None, stream=None):
+    """Softmax attention of q [T, q_heads, dim] (fp32 or bf16, any token and head strides) over the cached keys and
+    values of each row's sequence; query head h reads key head h // (q_heads // heads).  scale defaults to
+    dim ** -0.5; window > 0 limits a causal row to its last `window` positions; max_q, the largest number
+    of rows of a sequence, is a hint for the choice of kernel.  Rows that see nothing give zeros (lse -inf).
+
+    Returns out [T, q_heads, dim] of q's dtype, or (out, lse fp32 [T, q_heads]) with return_lse.  Calls that may
+    run at the same time need workspaces of their own."""
+    batch = _kv4_batch(cache, block_table, kv_lens, q_starts)
+    T, qts, qhs = _rows(q, "q", cache)
+    dt, heads = _xdt(q), q.shape[1]
+    shape = (T, heads, cache.dim)
+    out = torch.empty(shape, dtype=q.dtype, device=cache.device) if out is None else out
+    _need(out, "out", q.dtype, shape)
+    if lse is None and return_lse:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, heads))
+    nbytes = _native.load().bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch)
+    ws = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=cache.device) if ws is None else ws
+    _need(ws, "ws", torch.uint8)
+    if out.device != cache.device or ws.device != cache.device or (lse is not None and lse.device != cache.device):
+        raise ValueError(f"out, lse and ws must be on the cache's device {cache.device}")
+    scale = cache.dim ** -0.5 if scale is None else scale
+    _kv4_call(cache, "bitnet_kv4_attention", stream, q.data_ptr(), dt, T, heads, qts, qhs, cache._ref,
+              ctypes.byref(batch), scale, int(bool(causal)), window, max_q, out.data_ptr(),
+              None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return (out, lse) if return_lse else out
 
 
 def bitnet_get_last_device_status(stream=None) -> int:

@@ -28,6 +28,18 @@ ACT_INT4_ABSMEAN = 1
 F32 = 0
 BF16 = 1
 
+class Kv4Cache(ctypes.Structure):
+    """bitnet_kv4_cache_t"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_step", "v_step", "k_bos", "v_bos")] + [
+        ("pages", ctypes.c_int64), ("heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class Kv4Batch(ctypes.Structure):
+    """bitnet_kv4_batch_t"""
+    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 _LIBS: dict = {}  # loaded libraries by path
 
 
@@ -70,6 +82,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "bitnet_hbitlinear_forward_noalloc": (I, [P, I, I64, I64, P, F, I, I, P, P, I64, P, P]),
         "bitnet_act_quant_swiglu": (I, [P, P, I, I64, I64, P, F, I, I, P, P, P]),
         "bitnet_kv_quant": (I, [P, I, I64, I64, I64, I, F, P, P, P, P]),
+        "bitnet_kv4_write": (I, [P, P, I, I64, I64, I64, I64, I64, P, P, I, F, P]),
+        "bitnet_kv4_read": (I, [P, P, I64, P, P, I, P]),
+        "bitnet_kv4_attention_workspace_bytes": (SZ, [I64, I64, I64, I64, I64]),
+        "bitnet_kv4_attention": (I, [P, I, I64, I64, I64, I64, P, P, F, I, I64, I64, P, P, P, SZ, P]),
         "bitnet_ternary_gemm_ex": (I, [P, P, I, P, P, I64, I64, I64, P, I, P, P]),
         "bitnet_hbitlinear_forward_ex": (I, [P, I, I64, I64, P, F, I, I, P, P, I64, P, I, P, SZ, P]),
         "bitnet_hbitlinear_forward_swiglu": (I, [P, P, I, I64, I64, P, F, I, I, P, P, I64, P, P, SZ, P]),

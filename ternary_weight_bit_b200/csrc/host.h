@@ -113,6 +113,27 @@ cudaError_t forward_kernels(const void *X, bitnet_dtype_t xdt, int64_t M, int64_
 cudaError_t launch_kv_quant(const void *kv, bool bf16, int64_t BH, int64_t S, int D, int bits, float eps,
                             int8_t *codes, float *step, float *deq, cudaStream_t s);
 
+// The 4-bit paged KV cache (kv4.cu, kv4_attention.cu), as validated by kv4_abi.cu.
+struct Kv4Cache {
+    uint8_t *k_codes, *v_codes;
+    float *k_step, *v_step;
+    int8_t *k_bos, *v_bos;
+    int pages, heads, page_log2, dim;
+};
+struct Kv4Batch {
+    const int32_t *table, *lens, *starts;
+    int64_t table_stride;
+    int batch, max_pages;
+};
+cudaError_t launch_kv4_write(const void *k, const void *v, bool bf16, int64_t T, int64_t kts, int64_t khs, int64_t vts,
+                             int64_t vhs, const Kv4Cache &c, const Kv4Batch &bt, int bits, float eps, cudaStream_t s);
+cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &bt, int64_t T, void *k_out, void *v_out, bool bf16,
+                            cudaStream_t s);
+size_t kv4_attention_workspace(int64_t T, int q_heads, int heads, int dim, int batch);
+cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_heads, int64_t qts, int64_t qhs,
+                                 const Kv4Cache &c, const Kv4Batch &bt, float scale, bool causal, int64_t window,
+                                 int64_t max_q, void *out, float *lse, void *ws, cudaStream_t s);
+
 // Argument rules shared by every forward entry point (the workspace is checked by
 // each entry point): BITNET_OK or the status the call returns.
 bitnet_status_t validate_forward(const void *X, bitnet_dtype_t xdt, int64_t M, int64_t K, const float *gain,
