@@ -26,6 +26,7 @@ bitnet_status_t shape_of(const bitnet_kv4_cache_t *c, Kv4Cache *o) {
     if (log2 < 4 || (1 << log2) != c->page_size) return BITNET_ERR_UNSUPPORTED_SHAPE;
     if (c->heads < 1 || c->heads > kMaxHeads) return BITNET_ERR_UNSUPPORTED_SHAPE;
     if (c->pages < 0 || c->pages > INT32_MAX) return BITNET_ERR_INVALID_ARG;
+    if (c->pages * c->heads >= (((int64_t)1 << 32) - 64) >> log2) return BITNET_ERR_UNSUPPORTED_SHAPE;  // rows are counted in 32 bits
     *o = Kv4Cache{c->k_codes, c->v_codes, c->k_step, c->v_step, c->k_bos, c->v_bos, (int)c->pages, c->heads, log2,
                   c->dim};
     return BITNET_OK;

@@ -3,10 +3,14 @@
 // Method: bitnet_v2_engine.py page, BitNetV2Attention.forward on the fake-quantised keys and
 // values: s_t = scale * kstep_t * (q . kcode_t), out = sum_t e^(s_t) vstep_t vcode_t / sum_t e^(s_t).
 //
-// One CTA per (row, query head); each warp takes every fourth position with a running maximum,
-// sum and output, and the four are joined at the end.
+// Few rows to a sequence (decode, draft tokens): kv4_rows_kernel, below.  A sequence's rows
+// that share a key head (new tokens x query heads of the group) are one item of 8 * NT rows;
+// codes pass from memory to registers once and become fp16 operands of mma.sync there, with
+// the positions as the 16-side and the rows as the 8-side of the product, so that nothing is
+// padded for groups of up to 8.
 #include "kv4.cuh"
 
+#include <cuda_fp16.h>
 #include <math_constants.h>
 
 namespace bitnet {
@@ -14,123 +18,842 @@ namespace bitnet {
 namespace {
 
 constexpr int kWarps = 4;
-
+constexpr uint32_t kNowhere = 0xffffffffu;
+constexpr int kTile = 32;       // positions that a warp takes at a time
+constexpr int kMaxParts = 64;   // CTAs that may share an item on average
+constexpr int kMinTiles = 4;    // tiles that make a CTA of its own worth while
+// Weights are held as 2^(s - m + kOff), and a score may pass the running maximum m by kLag before
+// that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
+// for a finer second part.
 template <bool BF16>
-__device__ __forceinline__ float load1(const void *x, int64_t i) {
-    if constexpr (BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x)[i]);
-    else return reinterpret_cast<const float *>(x)[i];
-}
+constexpr float kOff = BF16 ? 6.0f : 13.0f;
+template <bool BF16>
+constexpr float kLag = BF16 ? 8.0f : 1.0f;
+constexpr float kNone = -3.0e38f;  // reference (m - kOff) of a row that has seen nothing yet
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-// The lane's E = D / 32 codes of a row.
-template <int E>
-__device__ __forceinline__ void codes_of(const uint8_t *row, int lane, float *y) {
-#pragma unroll
-    for (int j = 0; j < E / 2; ++j) {
-        const int b = row[lane * (E / 2) + j];
-        y[2 * j] = (float)((int)(b << 28) >> 28);
-        y[2 * j + 1] = (float)((int)(b << 24) >> 28);
+// A stage of a warp's ring: a tile's codes and steps, each lane's 16 (8, 4) bytes beside the others'.
+template <int D>
+struct Ring {
+    static constexpr uint32_t kKey = D / 8 * 32, kValue = D / 16 * 32;
+    static constexpr uint32_t kStage = 4 * kKey + 8 * kValue + 2 * 128;
+    static __host__ __device__ constexpr uint32_t key(int i) { return i * kKey; }
+    static __host__ __device__ constexpr uint32_t value(int i) { return 4 * kKey + i * kValue; }
+    static __host__ __device__ constexpr uint32_t step(int i) { return 4 * kKey + 8 * kValue + i * 128; }
+};
+// Tiles of a warp under way at a time: what fits the shared memory of an SM with kResident CTAs.
+template <int D, int NT>
+constexpr int kResident = D * NT == 64 || (D == 128 && NT == 1) ? 4 : (D == 64 ? 3 : 2);
+template <int D, int NT>
+constexpr int kStages = D == 128 && NT == 2 ? 5 : (D == 64 ? 5 : 3);
+template <int D, int NT>
+constexpr int kRowsSmem = (int)(kStages<D, NT> * Ring<D>::kStage) > 8 * NT * (D + 4) * 4 ? kWarps * (int)(kStages<D, NT> * Ring<D>::kStage)
+                                                                                      : kWarps * 8 * NT * (D + 4) * 4;
+
+struct RowsParams {
+    const void *q;
+    int64_t qts, qhs;
+    int q_heads, group;  // query heads, and those of one key head
+    int64_t T;
+    Kv4Cache c;
+    Kv4Batch bt;
+    float scale;
+    int causal;
+    int window;   // INT32_MAX: none
+    int rows_max; // sequences with more rows (new tokens x group) are another kernel's
+    int whole;    // 1: items are not split
+    void *out;
+    float *lse;
+    float *part;  // [grid][2][8 NT][D + 2]: output, reference, sum
+    int4 *head;   // [grid]: {sequence, key head * row tiles + row tile, CTAs, 1 if this CTA's part is the second}
+    int *status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t h2_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+__device__ __forceinline__ uint32_t h2(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+
+// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word as fp16 pairs.
+//
+// EXACT: the codes themselves.  (n ^ 8) = code + 8 goes into the mantissa of 1024, which is
+// then taken off (for the odd nibbles, which stand four bits higher, with a factor 1/16).
+// Otherwise: (code + 8) * 2^-24, and 16 times that for the odd nibbles, as the nibbles stand: as
+// fp16 they are subnormal numbers, which the tensor cores take as they are.  The caller
+// takes the 8 off the product (once per query for keys, once per tile for values) and
+// scales it.  9 instructions to a word become 5; the sum carries an 8 beside codes of
+// about 2.6, which costs it two bits, so fp32 calls do not do this.
+template <bool EXACT>
+__device__ __forceinline__ void halves(uint32_t w, uint32_t (&h)[4]) {
+    const uint32_t v = w >> 8;
+    if constexpr (EXACT) {
+        const __half2 off = __float2half2_rn(-1032.0f), off16 = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
+        h[0] = h2(__hadd2(as_h2((w & 0x000F000Fu) ^ 0x64086408u), off));
+        h[1] = h2(__hfma2(as_h2((w & 0x00F000F0u) ^ 0x64806480u), sixteenth, off16));
+        h[2] = h2(__hadd2(as_h2((v & 0x000F000Fu) ^ 0x64086408u), off));
+        h[3] = h2(__hfma2(as_h2((v & 0x00F000F0u) ^ 0x64806480u), sixteenth, off16));
+    } else {
+        h[0] = (w & 0x000F000Fu) ^ 0x00080008u;
+        h[1] = (w & 0x00F000F0u) ^ 0x00800080u;
+        h[2] = (v & 0x000F000Fu) ^ 0x00080008u;
+        h[3] = (v & 0x00F000F0u) ^ 0x00800080u;
     }
 }
+// A lane's copy of BYTES (4, 8 or a multiple of 16) into its own place in shared memory, where dst is the
+// warp's; zeros where !on (nothing is read then).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on) {
+    constexpr int N = BYTES < 16 ? BYTES : 16;
+    const int size = on ? N : 0;
+    dst += (threadIdx.x & 31) * N;
+    if constexpr (BYTES == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+    else if constexpr (BYTES == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+    else
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
+                         "l"(reinterpret_cast<const char *>(src) + 16 * i), "r"(size)
+                         : "memory");
+}
+// What copy_async<BYTES> put there.
+template <int BYTES>
+__device__ __forceinline__ void take(uint32_t src, uint32_t (&w)[BYTES / 4]) {
+    src += (threadIdx.x & 31) * (BYTES < 16 ? BYTES : 16);
+    if constexpr (BYTES == 4) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(src) : "memory");
+    } else if constexpr (BYTES == 8) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                         : "r"(src + i * 512)
+                         : "memory");
+    }
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-template <bool BF16, int D>
-__global__ void __launch_bounds__(32 * kWarps)
-kv4_attention_kernel(const void *__restrict__ q, int64_t qts, int64_t qhs, int q_heads, Kv4Cache c, Kv4Batch bt,
-                     float scale, int causal, int64_t window, void *__restrict__ out, float *__restrict__ lse,
-                     int *status) {
-    constexpr int E = D / 32;
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
+// A sequence's items: row tiles of R rows, and the tiles of positions that each may need.
+struct Seq {
+    int first;  // its first row among the call's
+    int base;   // position of that row
+    int cap;    // positions that the cache can hold of it
+    int rows, row_tiles, tiles;
+};
+template <int R>
+__device__ __forceinline__ Seq seq_of(const RowsParams &p, int b) {
+    Seq s;
+    s.first = max(0, __ldg(p.bt.starts + b));
+    const int n = max(0, __ldg(p.bt.starts + b + 1) - s.first);
+    const int len = max(0, __ldg(p.bt.lens + b));
+    s.base = len - n;
+    s.cap = (int)min((int64_t)len, (int64_t)p.bt.max_pages << p.c.page_log2);
+    // rows past the end of the tensors are nobody's
+    const int64_t rows = (int64_t)min((int64_t)n, max((int64_t)0, p.T - s.first)) * p.group;
+    s.rows = rows > p.rows_max ? 0 : (int)rows;
+    s.row_tiles = (s.rows + R - 1) / R;
+    // a row tile stands on at most R / group + 2 tokens
+    const int64_t span = min((int64_t)s.cap, (int64_t)p.window + R / p.group + 2);
+    s.tiles = max(1, (int)((span + kTile - 1) / kTile) + (p.window < len ? 1 : 0));
+    if (s.cap < len && s.rows > 0) record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
+    return s;
+}
+__device__ __forceinline__ int64_t weight(const RowsParams &p, const Seq &s) {
+    return (int64_t)s.row_tiles * p.c.heads * (p.whole ? 1 : s.tiles);
+}
+
+// Every CTA takes an equal run of all tiles of all items, in order; the run's first and last
+// item may be shared with its neighbours.  Their parts (output, reference, sum) go to the
+// workspace and kv4_join_kernel adds them up, in the order of the positions.
+//
+// Of a tile a warp computes S = K Q^T (positions x rows) with keys as the left operand, turns
+// the weights' 8 x 8 blocks with movmatrix into the right operand of O = V^T P
+// (dimensions x rows), whose left operand takes two positions' codes to a register.  Lane (g, t) =
+// (lane / 4, lane % 4) holds position 4 (g % 2) + g / 2 (+ 8) of a block of 16 as row g (+ 8),
+// so that the positions t, t + 4, t + 8, t + 12, which it needs of the values, lie in
+// neighbouring rows of the cache over t.
+//
+// Scores stand in units of log2.  The running maximum m of a row moves only when a score
+// passes it by more than kLag, so most tiles have no reduction and no rescaling; weights
+// 2^(s - m + kOff) stay below 2^15 and keep fp16's eleven bits down to 2^-21 of the maximum.
+// A tile's value steps are divided by their maximum, which scales the tile's product in fp32.
+// Queries are scaled by a power of two into [2^14, 2^15); bf16 queries are then exact in
+// fp16 down to 2^-28 of the row's maximum.  fp32 calls carry queries and weights as the
+// sum of two fp16 numbers (22 bits).
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(32 * kWarps, kResident<D, NT>)
+kv4_rows_kernel(const __grid_constant__ RowsParams p) {
+    constexpr int R = 8 * NT;
+    constexpr int KW = D / 32;  // words of keys per lane and position
+    constexpr int VW = D / 64;  // words of values per lane and position
+    constexpr int NP = BF16 ? 1 : 2;
+    constexpr bool EXACT = !BF16;  // keys
+    constexpr bool VEX = true;     // values
+    constexpr int LD = D + 4;
+    extern __shared__ __align__(16) float so[];  // [kWarps][R][LD] once the loop is done, the warps' rings before
+    __shared__ float sm[kWarps][R], sl[kWarps][R];
+    __shared__ int64_t scan[2 * kWarps];
+    __shared__ int start_b;
+    __shared__ int64_t start_off;
+
     pdl_launch_dependents();
     pdl_wait_prerequisites();
-    const int t = blockIdx.x, h = blockIdx.y, kh = h / (q_heads / c.heads);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int b, pos;
-    if (!kv4_locate(bt, t, b, pos)) return;
-    const int len = __ldg(bt.lens + b);
-    const int end = causal ? min(len, pos + 1) : len;
-    const int begin = (causal && window > 0) ? (int)max((int64_t)0, (int64_t)pos - window + 1) : 0;
-    float qv[E], o[E], m = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qv[e] = load1<BF16>(q, t * qts + h * qhs + lane * E + e);
-        o[e] = 0.0f;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(so) + warp * (kStages<D, NT> * Ring<D>::kStage);
+    const int B = p.bt.batch;
+
+    // this CTA's run [run, run_end) of the W tiles
+    const int per = (B + 32 * kWarps - 1) / (32 * kWarps);
+    int64_t mine = 0;
+    int64_t items = 0;
+    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
+        const Seq s = seq_of<R>(p, b);
+        mine += weight(p, s);
+        items += (int64_t)s.row_tiles * p.c.heads;
     }
-    for (int s = begin + warp; s < end; s += kWarps) {
-        const int page = kv4_page(c, bt, b, s, status);
-        if (page < 0) continue;
-        const int64_t row = kv4_rows(c, page, kh) + (s & ((1 << c.page_log2) - 1));
-        float kc[E], vc[E];
-        if (s == 0) {
+    int64_t before = mine, all_items = items;  // inclusive sums over the warp, then over the CTA
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                kc[e] = (float)c.k_bos[((int64_t)page * c.heads + kh) * D + lane * E + e];
-                vc[e] = (float)c.v_bos[((int64_t)page * c.heads + kh) * D + lane * E + e];
-            }
-        } else {
-            codes_of<E>(c.k_codes + row * (D / 2), lane, kc);
-            codes_of<E>(c.v_codes + row * (D / 2), lane, vc);
-        }
-        float z = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) z = fmaf(qv[e], kc[e], z);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-        z *= c.k_step[row] * scale;
-        const float m2 = fmaxf(m, z);
-        const float a = m == -CUDART_INF_F ? 0.0f : expf(m - m2), w = expf(z - m2);
-        const float wv = w * c.v_step[row];
-        l = fmaf(l, a, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, wv * vc[e]);
-        m = m2;
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, before, x);
+        if (lane >= x) before += y;
+        all_items += __shfl_xor_sync(0xffffffffu, all_items, x);
     }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    if (lane == 31) scan[warp] = before;
+    if (lane == 0) scan[kWarps + warp] = all_items;
     __syncthreads();
-    float top = -CUDART_INF_F, sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-    float f[kWarps];
+    int64_t W = 0;
+    items = 0;
+    before -= mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        f[w] = sm[w] == -CUDART_INF_F ? 0.0f : expf(sm[w] - top);
-        sum += f[w] * sl[w];
+        before += w < warp ? scan[w] : 0;
+        W += scan[w];
+        items += scan[kWarps + w];
     }
-    const int64_t base = ((int64_t)t * q_heads + h) * D;
-    for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
-        float y = 0.0f;
+    int64_t G = gridDim.x;
+    if (!p.whole) G = max((int64_t)1, min(min(G, items * kMaxParts), (W + kMinTiles - 1) / kMinTiles));
+    const int64_t cta = blockIdx.x;
+    const int64_t run0 = cta < G ? W * cta / G : W, run_end = cta < G ? W * (cta + 1) / G : W;
+    if (run0 >= run_end) {
+        if (!p.whole && tid == 0) p.head[cta] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    if (run0 >= before && run0 < before + mine) {
+        int b = tid * per;
+        int64_t off = run0 - before;
+        while (true) {
+            const int64_t w = weight(p, seq_of<R>(p, b));
+            if (off < w) break;
+            off -= w;
+            ++b;
+        }
+        start_b = b;
+        start_off = off;
+    }
+    __syncthreads();
+    int b = start_b;
+    int64_t off = start_off;
+
+    int64_t run = run0;
+    while (run < run_end) {
+        Seq s = seq_of<R>(p, b);
+        while (off >= weight(p, s)) {  // the next sequence with items
+            off -= weight(p, s);
+            s = seq_of<R>(p, ++b);
+        }
+        const int unit = p.whole ? 1 : s.tiles;
+        const int item = (int)(off / unit);  // key head * row tiles + row tile
+        const int kh = item / s.row_tiles, rt = item - kh * s.row_tiles;
+        const int lo = p.whole ? 0 : (int)(off - (int64_t)item * unit);
+        const int hi = p.whole ? s.tiles : (int)min((int64_t)s.tiles, lo + (run_end - run));
+        const bool whole = lo == 0 && hi == s.tiles;
+        if (!p.whole && run == run0 && tid == 0) {
+            // where this CTA's first part is the second of its item, it names the CTAs that share the item
+            int4 h = make_int4(0, 0, 0, 0);
+            const int64_t first = run0 - lo;  // of the item
+            if (lo > 0 && W * (cta - 1) / G <= first) {
+                int64_t last = cta;
+                while (W * (last + 1) / G < first + s.tiles) ++last;
+                h = make_int4(b, item, (int)(last - cta + 2), 1);
+            }
+            p.head[cta] = h;
+        }
+        const int row0 = rt * R, nrows = min(R, s.rows - row0);
+        const int q0 = s.first, base = s.base;
+        const int tok0 = row0 / p.group, tok1 = (row0 + nrows - 1) / p.group;
+        // positions that some row of the tile sees, and those that all see
+        const int end = p.causal ? min(s.cap, base + tok1 + 1) : s.cap;
+        const int begin = (int)max((int64_t)0, (int64_t)base + tok0 - p.window + 1) * p.causal;
+        const int all_end = p.causal ? base + tok0 + 1 : s.cap;
+        const int all_begin = p.causal ? (int)max((int64_t)0, (int64_t)base + tok1 - p.window + 1) : 0;
+        const int tile0 = begin / kTile;
+        // position 0 is kept at 8 bits: the item's first warp begins with it, and no tile has it
+        const int bos_page = lo == 0 && warp == 0 && begin == 0 && end > 0 ? kv4_page(p.c, p.bt, b, 0, p.status) : -1;
+
+        // queries: row 8 nt + g, dimensions t D/4 ...; bias and factor for the rows 2t, 2t + 1
+        uint32_t qf[NT][NP][KW][2][2];
+        float bias[NT][2], factor[NT][2], ref[NT][2];
+        int pos[NT][2];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) y += f[w] * so[w][d];
-        y = sum > 0.0f || sum != sum ? y / sum : 0.0f;
-        if constexpr (BF16) reinterpret_cast<__nv_bfloat16 *>(out)[base + d] = __float2bfloat16_rn(y);
-        else reinterpret_cast<float *>(out)[base + d] = y;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = row0 + 8 * nt + g;
+            const int tok = r / p.group;
+            const bool on = 8 * nt + g < nrows;
+            float x[D / 4];
+            const int64_t at = on ? (int64_t)(q0 + tok) * p.qts + (int64_t)(kh * p.group + r - tok * p.group) * p.qhs + t * (D / 4) : 0;
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 4; i += 8) {
+                if constexpr (BF16) {
+                    const uint4 u = on ? __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + at + i))
+                                       : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[i + 2 * j] = __uint_as_float(w[j] << 16);
+                        x[i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 u = on ? __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.q) + at + i + j))
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        x[i + j] = u.x, x[i + j + 1] = u.y, x[i + j + 2] = u.z, x[i + j + 3] = u.w;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i + j]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            float z0 = 0.0f;  // this row's product with position 0
+            if (bos_page >= 0) {
+                const int8_t *c8 = p.c.k_bos + ((int64_t)bos_page * p.c.heads + kh) * D + t * (D / 4);
+#pragma unroll
+                for (int i = 0; i < D / 4; i += 4) {
+                    const char4 u = *reinterpret_cast<const char4 *>(c8 + i);
+                    z0 = fmaf(x[i], u.x, z0), z0 = fmaf(x[i + 1], u.y, z0);
+                    z0 = fmaf(x[i + 2], u.z, z0), z0 = fmaf(x[i + 3], u.w, z0);
+                }
+                z0 += __shfl_xor_sync(0xffffffffu, z0, 1);
+                z0 += __shfl_xor_sync(0xffffffffu, z0, 2);
+                z0 *= p.scale * kLog2e * p.c.k_step[kv4_rows(p.c, bos_page, kh)];
+            }
+            // up = 2^(14 - exponent), kept inside the normal numbers (a row below 2^-112 is then scaled less)
+            const uint32_t up_bits = min(max(0x86000000u - (__float_as_uint(top) & 0x7f800000u), 0x07800000u), 0x7e800000u);
+            const float up = top > 0.0f ? __uint_as_float(up_bits) : 1.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) {
+                float y = x[i] * up;
+                if (!EXACT && (i & 1)) y *= 0.0625f;  // the odd nibbles stand 16 times as high
+                x[i] = y;
+                if (!EXACT) sum += __half2float(__float2half_rn(y)) * ((i & 1) ? 16.0f : 1.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < KW; ++j)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {  // product m takes nibbles m, m + 4 and m + 2, m + 6
+                        const float y0 = x[8 * j + m + 2 * e], y1 = x[8 * j + m + 2 * e + 4];
+                        qf[nt][0][j][m][e] = pack2(y0, y1);
+                        if constexpr (!BF16)
+                            qf[nt][NP - 1][j][m][e] = pack2(y0 - __half2float(__float2half_rn(y0)), y1 - __half2float(__float2half_rn(y1)));
+                    }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            // 2^24 undoes the subnormal codes; row n's values stand in lanes 4 n ...
+            const float f = p.scale * kLog2e * (1.0f / up) * (EXACT ? 1.0f : 0x1p24f);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                bias[nt][e] = -8.0f * 0x1p-24f * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+                factor[nt][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));
+                pos[nt][e] = base + (row0 + 8 * nt + 2 * t + e) / p.group;
+                const float z = __shfl_sync(0xffffffffu, z0, 4 * (2 * t + e));
+                const bool sees = bos_page >= 0 && (!p.causal || (pos[nt][e] >= 0 && pos[nt][e] < p.window));
+                ref[nt][e] = sees ? z - kOff<BF16> + (z - z) : kNone;  // an infinite score gives NaN
+            }
+        }
+
+        float l[NT][2], o[NT][D / 16][4];
+        const float bos_step = bos_page >= 0 ? p.c.v_step[kv4_rows(p.c, bos_page, kh)] : 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float w = ref[nt][c] == kNone ? 0.0f : (BF16 ? 0x1p6f : 0x1p13f);
+                l[nt][c] = g == 0 ? w : 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) o[nt][i][c] = o[nt][i][2 + c] = w == 0.0f ? 0.0f : w * bos_step;
+            }
+        if (bos_page >= 0) {
+            const int8_t *c8 = p.c.v_bos + ((int64_t)bos_page * p.c.heads + kh) * D + g * (D / 8);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const int d = 8 * (i >> 2) + 4 * ((i >> 1) & 1) + (i & 1);
+                const float f = VEX ? 1.0f : ((i & 1) ? 0x1p-20f : 0x1p-24f);
+                const float x = (float)c8[d] * f, y = (float)c8[d + 2] * f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) o[nt][i][0] *= x, o[nt][i][1] *= x, o[nt][i][2] *= y, o[nt][i][3] *= y;
+            }
+        }
+
+        // The warp's tiles lo + warp, + kWarps, ...: their blocks of 16 positions lie in the cache from these
+        // rows on, or kNowhere where no page holds them or nothing in them is seen.  Lane 2 i + h has half h
+        // of tile 16 n + i; the next 16 tiles' page numbers are on their way meanwhile.
+        const uint32_t mask = (1u << p.c.page_log2) - 1;
+        const int count = max(0, (min(hi, (end - tile0 * kTile + kTile - 1) / kTile) - lo - warp + kWarps - 1) / kWarps);
+        auto block_at = [&](int i) { return (tile0 + lo + warp + (i + (lane >> 1)) * kWarps) * kTile + 16 * (lane & 1); };
+        auto wanted = [&](int i) {
+            const int at = block_at(i);
+            return i + (lane >> 1) < count && at < end && at + 16 > begin;
+        };
+        auto page_of = [&](int i) {
+            const int n = block_at(i) >> p.c.page_log2;
+            return wanted(i) && n < p.bt.max_pages ? __ldg(p.bt.table + (int64_t)b * p.bt.table_stride + n) : -1;
+        };
+        auto rows_of = [&](int i, int page) {
+            if (!wanted(i)) return kNowhere;
+            if ((unsigned)page >= (unsigned)p.c.pages) {
+                record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
+                return kNowhere;
+            }
+            return (((uint32_t)page * p.c.heads + kh) << p.c.page_log2) + (block_at(i) & mask);
+        };
+        uint32_t rows = rows_of(0, page_of(0));
+        int pages = page_of(16);
+
+        const int rk = 4 * (g & 1) + (g >> 1);
+        const uint8_t *const k_base = p.c.k_codes + rk * (D / 2) + t * (D / 8);
+        const uint8_t *const v_base = p.c.v_codes + t * (D / 2) + g * (D / 16);
+        uint32_t valid = 0;  // two bits for each tile under way: whether its blocks lie somewhere
+        auto fetch = [&](int i, uint32_t slot) {  // the copies of the warp's tile i; one group, empty past the end
+            valid <<= 2;
+            if (i < count) {
+                if ((i & 15) == 0 && i > 0) {
+                    rows = rows_of(i, pages);
+                    pages = page_of(i + 16);
+                }
+                uint32_t r[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    r[h] = __shfl_sync(0xffffffffu, rows, 2 * (i & 15) + h);
+                    const bool on = r[h] != kNowhere;
+                    valid |= on << h;
+                    const uint64_t off = (uint64_t)(on ? r[h] : 0) * (D / 2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        copy_async<D / 8>(slot + Ring<D>::key(2 * h + e), k_base + off + e * 8 * (D / 2), on);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        copy_async<D / 16>(slot + Ring<D>::value(4 * h + e), v_base + off + e * 4 * (D / 2), on);
+                }
+                const uint32_t own = lane < 16 ? r[0] : r[1];
+                const bool on = own != kNowhere;
+                const uint32_t at = on ? own + (lane & 15) : 0;
+                copy_async<4>(slot + Ring<D>::step(0), p.c.k_step + at, on);
+                copy_async<4>(slot + Ring<D>::step(1), p.c.v_step + at, on);
+            }
+            copies_commit();
+        };
+        uint32_t slot_in = ring, slot_out = ring;
+        auto advance = [&](uint32_t &slot) {
+            slot += Ring<D>::kStage;
+            if (slot == ring + kStages<D, NT> * Ring<D>::kStage) slot = ring;
+        };
+#pragma unroll
+        for (int i = 0; i < kStages<D, NT> - 1; ++i) {
+            fetch(i, slot_in);
+            advance(slot_in);
+        }
+        for (int it = 0; it < count; ++it) {
+            const int at = (tile0 + lo + warp + it * kWarps) * kTile;
+            fetch(it + kStages<D, NT> - 1, slot_in);
+            advance(slot_in);
+            copies_wait<kStages<D, NT> - 1>();
+
+            // S = K Q^T
+            float sc[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    sc[nt][h][0] = sc[nt][h][2] = EXACT ? 0.0f : bias[nt][0];
+                    sc[nt][h][1] = sc[nt][h][3] = EXACT ? 0.0f : bias[nt][1];
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t kw[2][KW];
+                take<D / 8>(slot_out + Ring<D>::key(2 * h), kw[0]);
+                take<D / 8>(slot_out + Ring<D>::key(2 * h + 1), kw[1]);
+#pragma unroll
+                for (int j = 0; j < KW; ++j) {
+                    uint32_t x[4], y[4];
+                    halves<EXACT>(kw[0][j], x);
+                    halves<EXACT>(kw[1][j], y);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k2 = NP - 1; k2 >= 0; --k2) {
+                            mma_f16(sc[nt][h], x[0], y[0], x[2], y[2], qf[nt][k2][j][0][0], qf[nt][k2][j][0][1]);
+                            mma_f16(sc[nt][h], x[1], y[1], x[3], y[3], qf[nt][k2][j][1][0], qf[nt][k2][j][1][1]);
+                        }
+                }
+            }
+            // the lane's own position: its key step, and its value step over a power of two that
+            // no step of the tile is twice as large as (one that is not finite stays with its position)
+            const int own = at + lane;
+            uint32_t steps[2][1];
+            take<4>(slot_out + Ring<D>::step(0), steps[0]);
+            take<4>(slot_out + Ring<D>::step(1), steps[1]);
+            const bool live = own >= max(begin, 1) && own < end && (valid >> (2 * (kStages<D, NT> - 1) + (lane >> 4)) & 1);
+            const float kstep = live ? __uint_as_float(steps[0][0]) : 0.0f, vstep = live ? __uint_as_float(steps[1][0]) : 0.0f;
+            const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
+            const uint32_t vbits = __float_as_uint(vstep) & 0x7f800000u;
+            const uint32_t vexp = min(max(__reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u), 0x0d000000u), 0x7e000000u);
+            const float vtop = __uint_as_float(vexp);
+            const float vrel = vstep * __uint_as_float(0x7f000000u - vexp);
+            const bool edge = at < all_begin || at + kTile > all_end || live_bits != 0xffffffffu;
+
+            // scores less the reference; where one is too far above it, the references move first
+            float st[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) st[h][e] = __shfl_sync(0xffffffffu, kstep, 16 * h + 8 * e + rk);
+            float y[NT][2][4];
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float &z = y[nt][h][2 * e + c];
+                                z = fmaf(sc[nt][h][2 * e + c], st[h][e] * factor[nt][c], -ref[nt][c]);
+                                if (edge) {
+                                    const int i = 16 * h + 8 * e + rk;  // position of rows g and g + 8
+                                    const bool sees = (live_bits >> i & 1) && (!p.causal || (at + i <= pos[nt][c] &&
+                                                                                             pos[nt][c] - (at + i) < p.window));
+                                    if (!sees) z = -CUDART_INF_F;
+                                }
+                                top = fmaxf(top, z);
+                            }
+                if (pass == 1 || !__any_sync(0xffffffffu, top > kOff<BF16> + kLag<BF16>)) break;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float most = -CUDART_INF_F;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (y[nt][h][2 * e + c] != -CUDART_INF_F)
+                                    most = fmaxf(most, sc[nt][h][2 * e + c] * (st[h][e] * factor[nt][c]));
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+                        most = fmaxf(most - kOff<BF16>, ref[nt][c]);
+                        const float a = ex2(ref[nt][c] - most);
+                        ref[nt][c] = most;
+                        l[nt][c] *= a;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) o[nt][i][c] *= a, o[nt][i][2 + c] *= a;
+                    }
+            }
+            // weights, times the values' steps, as the right operand
+            uint32_t pf[NT][NP][2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float vr = __shfl_sync(0xffffffffu, vrel, 16 * h + 8 * e + rk);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float w[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float x = ex2(y[nt][h][2 * e + c]);
+                            l[nt][c] += x;
+                            w[c] = x * vr;
+                            if (edge && y[nt][h][2 * e + c] == -CUDART_INF_F) w[c] = 0.0f;  // whatever the step
+                        }
+                        const uint32_t hi2 = pack2(w[0], w[1]);
+                        pf[nt][0][h][e] = transpose8(hi2);
+                        if constexpr (!BF16) {
+                            const float2 f2 = __half22float2(as_h2(hi2));
+                            pf[nt][NP - 1][h][e] = transpose8(pack2(w[0] - f2.x, w[1] - f2.y));
+                        }
+                    }
+                }
+            // O = O + V^T P
+            float eight[NT][4];
+            if constexpr (!VEX) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    eight[nt][0] = eight[nt][1] = eight[nt][2] = eight[nt][3] = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        mma_f16(eight[nt], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, pf[nt][0][h][0], pf[nt][0][h][1]);
+                }
+            }
+            uint32_t vw[8][VW];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) take<D / 16>(slot_out + Ring<D>::value(i), vw[i]);
+#pragma unroll
+            for (int j = 0; j < VW; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {  // nibbles 0 .. 3 or 4 .. 7 of the word
+                    uint32_t x[2][2][4];       // [block][positions t, t + 4 or t + 8, t + 12][nibble]
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            halves<VEX>(__byte_perm(vw[4 * h + 2 * e][j], vw[4 * h + 2 * e + 1][j], u ? 0x7632 : 0x5410), x[h][e]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int odd = 0; odd < 2; ++odd) {
+                            float acc[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[i] = VEX ? 0.0f : eight[nt][i] * (odd ? 16.0f : 1.0f);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int k2 = NP - 1; k2 >= 0; --k2)
+                                    mma_f16(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2], pf[nt][k2][h][0],
+                                            pf[nt][k2][h][1]);
+                            float(&dst)[4] = o[nt][4 * j + 2 * u + odd];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) dst[i] = fmaf(vtop, acc[i], dst[i]);
+                        }
+                }
+            advance(slot_out);
+        }
+        copies_wait<0>();
+        __syncthreads();  // every warp is done with its ring
+
+        // join the warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+                const int n = 8 * nt + 2 * t + c;
+                if (g == 0) sm[warp][n] = ref[nt][c], sl[warp][n] = l[nt][c];
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const float f = VEX ? 1.0f : ((i & 1) ? 0x1p20f : 0x1p24f);
+                    const int d = g * (D / 8) + 8 * (i >> 2) + 4 * ((i >> 1) & 1) + (i & 1);
+                    so[(warp * R + n) * LD + d] = o[nt][i][c] * f;
+                    so[(warp * R + n) * LD + d + 2] = o[nt][i][2 + c] * f;
+                }
+            }
+        __syncthreads();
+        float *part = p.part + ((cta * 2 + (lo > 0 ? 0 : 1)) * R) * (D + 2);
+        for (int i = tid; i < nrows * (D / 4); i += 32 * kWarps) {
+            const int n = i / (D / 4), d = 4 * (i % (D / 4));
+            float top = kNone, sum = 0.0f;
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w][n]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(sm[w][n] - top);
+                const float4 x = *reinterpret_cast<const float4 *>(so + (w * R + n) * LD + d);
+                sum = fmaf(f, sl[w][n], sum);
+                y.x = fmaf(f, x.x, y.x), y.y = fmaf(f, x.y, y.y), y.z = fmaf(f, x.z, y.z), y.w = fmaf(f, x.w, y.w);
+            }
+            if (!whole) {
+                float *dst = part + n * (D + 2);
+                *reinterpret_cast<float2 *>(dst + d) = make_float2(y.x, y.y);
+                *reinterpret_cast<float2 *>(dst + d + 2) = make_float2(y.z, y.w);
+                if (d == 0) dst[D] = top, dst[D + 1] = sum;
+                continue;
+            }
+            const int r = row0 + n, tok = r / p.group;
+            const int64_t at = (int64_t)(q0 + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            if constexpr (BF16)
+                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.out) + at * D + d) = make_uint2(
+                    h2_bf16(y.x * inv, y.y * inv), h2_bf16(y.z * inv, y.w * inv));
+            else
+                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + at * D + d) =
+                    make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+            if (p.lse && d == 0) p.lse[at] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+        }
+        __syncthreads();
+        const int64_t done = p.whole ? 1 : hi - lo;
+        run += done;
+        off += done;
     }
-    if (lse && threadIdx.x == 0) lse[(int64_t)t * q_heads + h] = sum > 0.0f || sum != sum ? top + logf(sum) : -CUDART_INF_F;
+}
+
+// Joins the parts of the items that several CTAs of kv4_rows_kernel shared: one CTA to each of
+// that kernel's, which finds in p.head whether an item is its to join.
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ RowsParams p) {
+    constexpr int R = 8 * NT;
+    constexpr int PER = D / 32;
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
+    const int cta = blockIdx.x;
+    const int4 h = p.head[cta];
+    if (h.w == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Seq s = seq_of<R>(p, h.x);
+    const int kh = h.y / s.row_tiles, row0 = (h.y - kh * s.row_tiles) * R;
+    const int nrows = min(R, s.rows - row0);
+    const int q0 = s.first;
+    for (int n = warp; n < nrows; n += 8) {
+        // part 0 lies in the CTA before, as the one it began; the others continue it
+        auto part = [&](int i) { return p.part + (((int64_t)(cta - 1 + i) * 2 + (i == 0 ? 1 : 0)) * R + n) * (D + 2); };
+        float top = kNone;
+        for (int i = lane; i < h.z; i += 32) top = fmaxf(top, part(i)[D]);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        float sum = 0.0f, y[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) y[e] = 0.0f;
+#pragma unroll 8
+        for (int i = 0; i < h.z; ++i) {
+            const float *x = part(i);
+            const float m = x[D], l = x[D + 1];
+            const float f = ex2(m - top);
+            sum = fmaf(f, l, sum);
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(x + lane * 2 + e * 32);
+                y[e] = fmaf(f, v.x, y[e]);
+                y[e + 1] = fmaf(f, v.y, y[e + 1]);
+            }
+        }
+        const int r = row0 + n, tok = r / p.group;
+        const int64_t at = (int64_t)(q0 + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2) {
+            const int64_t d = at * D + lane * 2 + e * 32;
+            if constexpr (BF16) *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + d) = h2_bf16(y[e] * inv, y[e + 1] * inv);
+            else *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.out) + d) = make_float2(y[e] * inv, y[e + 1] * inv);
+        }
+        if (p.lse && lane == 0) p.lse[at] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+    }
+}
+
+constexpr int kMaxGrid = 4 * 148 * 4;
+
+template <typename... P, typename... A>
+cudaError_t launch_one(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Dynamic shared memory above 48 KB has to be allowed once per kernel and device.
+cudaError_t allow_smem(const void *kernel, int bytes, bool (&done)[kMaxDevices]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < kMaxDevices) done[dev] = true;
+    return e;
+}
+
+template <int D, int NT, bool BF16>
+cudaError_t launch_rows(RowsParams p, int64_t T, void *ws, cudaStream_t s) {
+    constexpr size_t smem = kRowsSmem<D, NT>;
+    static bool allowed[kMaxDevices] = {};
+    const cudaError_t e = allow_smem((const void *)kv4_rows_kernel<D, NT, BF16>, (int)smem, allowed);
+    if (e != cudaSuccess) return e;
+    const int slots = sm_count() * kResident<D, NT>;
+    const int grid = slots;
+    p.whole = 0;
+    p.head = static_cast<int4 *>(ws);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + (size_t)grid * sizeof(int4));
+    const cudaError_t r = launch_one(kv4_rows_kernel<D, NT, BF16>, grid, 32 * kWarps, smem, s, p);
+    if (r != cudaSuccess) return r;
+    return launch_one(kv4_join_kernel<D, NT, BF16>, grid, 256, 0, s, p);
 }
 
 }  // namespace
 
-size_t kv4_attention_workspace(int64_t, int, int, int, int) { return 256; }
+size_t kv4_attention_workspace(int64_t, int, int, int dim, int) {
+    // the largest of the kernels': a slot and two parts of 8 NT rows to a CTA
+    auto need = [&](int resident, int nt) {
+        return (size_t)sm_count() * resident * (sizeof(int4) + 2 * 8 * nt * (size_t)(dim + 2) * 4);
+    };
+    const size_t one = dim == 64 ? need(kResident<64, 1>, 1) : (dim == 128 ? need(kResident<128, 1>, 1) : need(kResident<256, 1>, 1));
+    const size_t two = dim == 64 ? need(kResident<64, 2>, 2) : (dim == 128 ? need(kResident<128, 2>, 2) : 0);
+    return ((one > two ? one : two) + 255) & ~(size_t)255;
+}
 
 cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_heads, int64_t qts, int64_t qhs,
                                  const Kv4Cache &c, const Kv4Batch &bt, float scale, bool causal, int64_t window,
-                                 int64_t, void *out, float *lse, void *, cudaStream_t s) {
-    auto go = [&](auto kernel) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)T, (unsigned)q_heads);
-        cfg.blockDim = dim3(32 * kWarps);
-        cfg.stream = s;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kernel, q, qts, qhs, q_heads, c, bt, scale, (int)causal, window, out, lse,
-                                  device_status_ptr());
-    };
-    if (c.dim == 64) return bf16 ? go(kv4_attention_kernel<true, 64>) : go(kv4_attention_kernel<false, 64>);
-    if (c.dim == 128) return bf16 ? go(kv4_attention_kernel<true, 128>) : go(kv4_attention_kernel<false, 128>);
-    return bf16 ? go(kv4_attention_kernel<true, 256>) : go(kv4_attention_kernel<false, 256>);
+                                 int64_t max_q, void *out, float *lse, void *ws, cudaStream_t s) {
+    RowsParams p = {};
+    p.q = q, p.qts = qts, p.qhs = qhs, p.q_heads = q_heads, p.group = q_heads / c.heads, p.T = T;
+    p.c = c, p.bt = bt, p.scale = scale, p.causal = causal;
+    p.window = window > 0 && window < INT32_MAX ? (int)window : INT32_MAX;
+    p.rows_max = INT32_MAX;
+    p.out = out, p.lse = lse, p.status = device_status_ptr();
+    const int64_t rows = (max_q > 0 ? max_q : T) * p.group;
+    const bool two = rows > 8;
+    if (c.dim == 64) {
+        if (two) return bf16 ? launch_rows<64, 2, true>(p, T, ws, s) : launch_rows<64, 2, false>(p, T, ws, s);
+        return bf16 ? launch_rows<64, 1, true>(p, T, ws, s) : launch_rows<64, 1, false>(p, T, ws, s);
+    }
+    if (c.dim == 128) {
+        if (two) return bf16 ? launch_rows<128, 2, true>(p, T, ws, s) : launch_rows<128, 2, false>(p, T, ws, s);
+        return bf16 ? launch_rows<128, 1, true>(p, T, ws, s) : launch_rows<128, 1, false>(p, T, ws, s);
+    }
+    return bf16 ? launch_rows<256, 1, true>(p, T, ws, s) : launch_rows<256, 1, false>(p, T, ws, s);
 }
 
 }  // namespace bitnet

@@ -82,15 +82,22 @@ def attention(q, k, v, scale, causal, window):
     return out, lse.T, top.T, mass
 
 
-def attention_bounds(out, top, mass, dim, length, dtype):
+def attention_bounds(out, top, mass, dim, length, dtype, largest):
     """How far out and lse may be off.  A score is a sum of dim products in fp32 and some scalings: its error is a
     sum of about dim + 8 independent roundings of at most 2 U (the tensor cores cut where they add) relative to
     sum |q k|, taken at 2 sqrt(dim) + 8 times 2 U.  A weight's relative error is that of its score (twice: once in
     the numerator, once in the sum) and some roundings of the exponential; the sums over positions add
-    2 sqrt(length) roundings.  bf16 calls round weights to fp16 (2^-11) and the output to bf16 (2^-8)."""
+    2 sqrt(length) roundings.  bf16 calls round weights to fp16 (2^-11) and the output to bf16 (2^-8).
+
+    Weights far below the row's largest reach the end of fp16's range.  Weights w step / 2^e, with 2^e at most the
+    largest step among 32 neighbours, are held as multiples of 2^-24 where the largest w is at least 2^6 (bf16 calls) or
+    2^13 (fp32 calls, in their second part): each is off by at most 2^-25, so that of the largest by 2^-31 (2^-38),
+    times 2^e and a code of at most 8 (127 at position 0).  A row with the step 2^e has a code of 1 or
+    more, so 2^e is at most the largest |value| of the sequence (`largest`)."""
     score = 2 * U * (2 * math.sqrt(dim) + 8) * top
     rel = 2 * score + (2 * math.sqrt(length) + 32) * U
     if dtype == torch.bfloat16:
         rel = rel + 2.0 ** -11
     err = rel[..., None] * mass + out.abs() * (2.0 ** -8 if dtype == torch.bfloat16 else U) + 1e-37
+    err = err + (2.0 ** -31 if dtype == torch.bfloat16 else 2.0 ** -38) * (8 * length + 127) * largest
     return err, score + (2 * math.sqrt(length) + 32) * U
