@@ -68,6 +68,7 @@ struct RowsParams {
     float *part;  // [grid][2][8 NT][D + 2]: output, reference, sum
     int4 *head;   // [grid]: {sequence, key head * row tiles + row tile, CTAs, 1 if this CTA's part is the second}
     int *status;
+    uint32_t magic[2];  // see halves()
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -80,6 +81,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -97,53 +105,43 @@ __device__ __forceinline__ uint32_t h2_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t h2(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 
-// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word as fp16 pairs.
-//
-// EXACT: the codes themselves.  (n ^ 8) = code + 8 goes into the mantissa of 1024, which is
-// then taken off (for the odd nibbles, which stand four bits higher, with a factor 1/16).
-// Otherwise: (code + 8) * 2^-24, and 16 times that for the odd nibbles, as the nibbles stand: as
-// fp16 they are subnormal numbers, which the tensor cores take as they are.  The caller
-// takes the 8 off the product (once per query for keys, once per tile for values) and
-// scales it.  9 instructions to a word become 5; the sum carries an 8 beside codes of
-// about 2.6, which costs it two bits, so fp32 calls do not do this.
-template <bool EXACT>
-__device__ __forceinline__ void halves(uint32_t w, uint32_t (&h)[4]) {
+// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word as pairs of codes in fp16: (n ^ 8) = code + 8 goes into
+// the mantissa of 1024, which is then taken off (for the odd nibbles, which stand four bits
+// higher, with a factor 1/16).  magic is {0x64086408, 0x64806480}, in registers: a logic
+// instruction takes one constant, so that with two of them each half would cost two (measured: 291
+// to a tile instead of 165, on the pipe that binds).
+__device__ __forceinline__ void halves(uint32_t w, const uint32_t (&magic)[2], uint32_t (&h)[4]) {
     const uint32_t v = w >> 8;
-    if constexpr (EXACT) {
-        const __half2 off = __float2half2_rn(-1032.0f), off16 = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
-        h[0] = h2(__hadd2(as_h2((w & 0x000F000Fu) ^ 0x64086408u), off));
-        h[1] = h2(__hfma2(as_h2((w & 0x00F000F0u) ^ 0x64806480u), sixteenth, off16));
-        h[2] = h2(__hadd2(as_h2((v & 0x000F000Fu) ^ 0x64086408u), off));
-        h[3] = h2(__hfma2(as_h2((v & 0x00F000F0u) ^ 0x64806480u), sixteenth, off16));
-    } else {
-        h[0] = (w & 0x000F000Fu) ^ 0x00080008u;
-        h[1] = (w & 0x00F000F0u) ^ 0x00800080u;
-        h[2] = (v & 0x000F000Fu) ^ 0x00080008u;
-        h[3] = (v & 0x00F000F0u) ^ 0x00800080u;
-    }
+    const __half2 off = __float2half2_rn(-1032.0f), off16 = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
+    h[0] = h2(__hadd2(as_h2((w & 0x000F000Fu) ^ magic[0]), off));
+    h[1] = h2(__hfma2(as_h2((w & 0x00F000F0u) ^ magic[1]), sixteenth, off16));
+    h[2] = h2(__hadd2(as_h2((v & 0x000F000Fu) ^ magic[0]), off));
+    h[3] = h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth, off16));
 }
+
 // A lane's copy of BYTES (4, 8 or a multiple of 16) into its own place in shared memory, where dst is the
 // warp's; zeros where !on (nothing is read then).
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int lane, bool on) {
     constexpr int N = BYTES < 16 ? BYTES : 16;
-    const int size = on ? N : 0;
-    dst += (threadIdx.x & 31) * N;
-    if constexpr (BYTES == 4)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
-    else if constexpr (BYTES == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
-    else
 #pragma unroll
-        for (int i = 0; i < BYTES / 16; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
-                         "l"(reinterpret_cast<const char *>(src) + 16 * i), "r"(size)
+    for (int i = 0; i < BYTES / N; ++i) {
+        const uint32_t to = dst + lane * N + i * 512;
+        const char *from = reinterpret_cast<const char *>(src) + 16 * i;
+        if constexpr (N == 16)
+            asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.cg.shared.global [%0], [%1], 16, p;}" ::"r"(to), "l"(from),
+                         "r"((uint32_t)on)
                          : "memory");
+        else
+            asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.ca.shared.global [%0], [%1], %3, p;}" ::"r"(to), "l"(from),
+                         "r"((uint32_t)on), "n"(N)
+                         : "memory");
+    }
 }
 // What copy_async<BYTES> put there.
 template <int BYTES>
-__device__ __forceinline__ void take(uint32_t src, uint32_t (&w)[BYTES / 4]) {
-    src += (threadIdx.x & 31) * (BYTES < 16 ? BYTES : 16);
+__device__ __forceinline__ void take(uint32_t src, int lane, uint32_t (&w)[BYTES / 4]) {
+    src += lane * (BYTES < 16 ? BYTES : 16);
     if constexpr (BYTES == 4) {
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(src) : "memory");
     } else if constexpr (BYTES == 8) {
@@ -217,8 +215,6 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
     constexpr int KW = D / 32;  // words of keys per lane and position
     constexpr int VW = D / 64;  // words of values per lane and position
     constexpr int NP = BF16 ? 1 : 2;
-    constexpr bool EXACT = !BF16;  // keys
-    constexpr bool VEX = true;     // values
     constexpr int LD = D + 4;
     extern __shared__ __align__(16) float so[];  // [kWarps][R][LD] once the loop is done, the warps' rings before
     __shared__ float sm[kWarps][R], sl[kWarps][R];
@@ -232,6 +228,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(so) + warp * (kStages<D, NT> * Ring<D>::kStage);
     const int B = p.bt.batch;
+    const uint32_t magic[2] = {p.magic[0], p.magic[1]};
 
     // this CTA's run [run, run_end) of the W tiles
     const int per = (B + 32 * kWarps - 1) / (32 * kWarps);
@@ -321,9 +318,9 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         // position 0 is kept at 8 bits: the item's first warp begins with it, and no tile has it
         const int bos_page = lo == 0 && warp == 0 && begin == 0 && end > 0 ? kv4_page(p.c, p.bt, b, 0, p.status) : -1;
 
-        // queries: row 8 nt + g, dimensions t D/4 ...; bias and factor for the rows 2t, 2t + 1
+        // queries: row 8 nt + g, dimensions t D/4 ...; factor and reference for the rows 2t, 2t + 1
         uint32_t qf[NT][NP][KW][2][2];
-        float bias[NT][2], factor[NT][2], ref[NT][2];
+        float factor[NT][2], ref[NT][2];
         int pos[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -373,14 +370,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             // up = 2^(14 - exponent), kept inside the normal numbers (a row below 2^-112 is then scaled less)
             const uint32_t up_bits = min(max(0x86000000u - (__float_as_uint(top) & 0x7f800000u), 0x07800000u), 0x7e800000u);
             const float up = top > 0.0f ? __uint_as_float(up_bits) : 1.0f;
-            float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) {
-                float y = x[i] * up;
-                if (!EXACT && (i & 1)) y *= 0.0625f;  // the odd nibbles stand 16 times as high
-                x[i] = y;
-                if (!EXACT) sum += __half2float(__float2half_rn(y)) * ((i & 1) ? 16.0f : 1.0f);
-            }
+            for (int i = 0; i < D / 4; ++i) x[i] *= up;
 #pragma unroll
             for (int j = 0; j < KW; ++j)
 #pragma unroll
@@ -392,13 +383,9 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                         if constexpr (!BF16)
                             qf[nt][NP - 1][j][m][e] = pack2(y0 - __half2float(__float2half_rn(y0)), y1 - __half2float(__float2half_rn(y1)));
                     }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            // 2^24 undoes the subnormal codes; row n's values stand in lanes 4 n ...
-            const float f = p.scale * kLog2e * (1.0f / up) * (EXACT ? 1.0f : 0x1p24f);
+            const float f = p.scale * kLog2e * (1.0f / up);  // of row n in lanes 4 n ...
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                bias[nt][e] = -8.0f * 0x1p-24f * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
                 factor[nt][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));
                 pos[nt][e] = base + (row0 + 8 * nt + 2 * t + e) / p.group;
                 const float z = __shfl_sync(0xffffffffu, z0, 4 * (2 * t + e));
@@ -423,8 +410,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 const int d = 8 * (i >> 2) + 4 * ((i >> 1) & 1) + (i & 1);
-                const float f = VEX ? 1.0f : ((i & 1) ? 0x1p-20f : 0x1p-24f);
-                const float x = (float)c8[d] * f, y = (float)c8[d + 2] * f;
+                const float x = (float)c8[d], y = (float)c8[d + 2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) o[nt][i][0] *= x, o[nt][i][1] *= x, o[nt][i][2] *= y, o[nt][i][3] *= y;
             }
@@ -475,16 +461,16 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                     const uint64_t off = (uint64_t)(on ? r[h] : 0) * (D / 2);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        copy_async<D / 8>(slot + Ring<D>::key(2 * h + e), k_base + off + e * 8 * (D / 2), on);
+                        copy_async<D / 8>(slot + Ring<D>::key(2 * h + e), k_base + off + e * 8 * (D / 2), lane, on);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        copy_async<D / 16>(slot + Ring<D>::value(4 * h + e), v_base + off + e * 4 * (D / 2), on);
+                        copy_async<D / 16>(slot + Ring<D>::value(4 * h + e), v_base + off + e * 4 * (D / 2), lane, on);
                 }
                 const uint32_t own = lane < 16 ? r[0] : r[1];
                 const bool on = own != kNowhere;
                 const uint32_t at = on ? own + (lane & 15) : 0;
-                copy_async<4>(slot + Ring<D>::step(0), p.c.k_step + at, on);
-                copy_async<4>(slot + Ring<D>::step(1), p.c.v_step + at, on);
+                copy_async<4>(slot + Ring<D>::step(0), p.c.k_step + at, lane, on);
+                copy_async<4>(slot + Ring<D>::step(1), p.c.v_step + at, lane, on);
             }
             copies_commit();
         };
@@ -507,27 +493,23 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             // S = K Q^T
             float sc[NT][2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    sc[nt][h][0] = sc[nt][h][2] = EXACT ? 0.0f : bias[nt][0];
-                    sc[nt][h][1] = sc[nt][h][3] = EXACT ? 0.0f : bias[nt][1];
-                }
-#pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t kw[2][KW];
-                take<D / 8>(slot_out + Ring<D>::key(2 * h), kw[0]);
-                take<D / 8>(slot_out + Ring<D>::key(2 * h + 1), kw[1]);
+                take<D / 8>(slot_out + Ring<D>::key(2 * h), lane, kw[0]);
+                take<D / 8>(slot_out + Ring<D>::key(2 * h + 1), lane, kw[1]);
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     uint32_t x[4], y[4];
-                    halves<EXACT>(kw[0][j], x);
-                    halves<EXACT>(kw[1][j], y);
+                    halves(kw[0][j], magic, x);
+                    halves(kw[1][j], magic, y);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k2 = NP - 1; k2 >= 0; --k2) {
-                            mma_f16(sc[nt][h], x[0], y[0], x[2], y[2], qf[nt][k2][j][0][0], qf[nt][k2][j][0][1]);
+                            if (j == 0 && k2 == NP - 1)
+                                mma_f16_first(sc[nt][h], x[0], y[0], x[2], y[2], qf[nt][k2][j][0][0], qf[nt][k2][j][0][1]);
+                            else
+                                mma_f16(sc[nt][h], x[0], y[0], x[2], y[2], qf[nt][k2][j][0][0], qf[nt][k2][j][0][1]);
                             mma_f16(sc[nt][h], x[1], y[1], x[3], y[3], qf[nt][k2][j][1][0], qf[nt][k2][j][1][1]);
                         }
                 }
@@ -536,8 +518,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             // no step of the tile is twice as large as (one that is not finite stays with its position)
             const int own = at + lane;
             uint32_t steps[2][1];
-            take<4>(slot_out + Ring<D>::step(0), steps[0]);
-            take<4>(slot_out + Ring<D>::step(1), steps[1]);
+            take<4>(slot_out + Ring<D>::step(0), lane, steps[0]);
+            take<4>(slot_out + Ring<D>::step(1), lane, steps[1]);
             const bool live = own >= max(begin, 1) && own < end && (valid >> (2 * (kStages<D, NT> - 1) + (lane >> 4)) & 1);
             const float kstep = live ? __uint_as_float(steps[0][0]) : 0.0f, vstep = live ? __uint_as_float(steps[1][0]) : 0.0f;
             const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
@@ -548,33 +530,33 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             const bool edge = at < all_begin || at + kTile > all_end || live_bits != 0xffffffffu;
 
             // scores less the reference; where one is too far above it, the references move first
-            float st[2][2];
+            float st[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 4; ++i) st[i] = __shfl_sync(0xffffffffu, kstep, 8 * i + rk);
+            float y[NT][8];  // element i: position 8 (i / 2) + rk of the tile, row 2 t + i % 2
+            auto hide = [&](float(&z)[NT][8]) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) st[h][e] = __shfl_sync(0xffffffffu, kstep, 16 * h + 8 * e + rk);
-            float y[NT][2][4];
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = 8 * (i >> 1) + rk, s = at + j;
+                        const bool sees = (live_bits >> j & 1) && (!p.causal || (s <= pos[nt][i & 1] && pos[nt][i & 1] - s < p.window));
+                        if (!sees) z[nt][i] = -CUDART_INF_F;
+                    }
+            };
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
-                float top = -CUDART_INF_F;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int i = 0; i < 8; ++i)
+                        y[nt][i] = fmaf(sc[nt][i >> 2][i & 3], st[i >> 1] * factor[nt][i & 1], -ref[nt][i & 1]);
+                if (edge) hide(y);
+                float top = y[0][0];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                float &z = y[nt][h][2 * e + c];
-                                z = fmaf(sc[nt][h][2 * e + c], st[h][e] * factor[nt][c], -ref[nt][c]);
-                                if (edge) {
-                                    const int i = 16 * h + 8 * e + rk;  // position of rows g and g + 8
-                                    const bool sees = (live_bits >> i & 1) && (!p.causal || (at + i <= pos[nt][c] &&
-                                                                                             pos[nt][c] - (at + i) < p.window));
-                                    if (!sees) z = -CUDART_INF_F;
-                                }
-                                top = fmaxf(top, z);
-                            }
+                    for (int i = 0; i < 8; ++i) top = fmaxf(top, y[nt][i]);
                 if (pass == 1 || !__any_sync(0xffffffffu, top > kOff<BF16> + kLag<BF16>)) break;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -582,11 +564,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                     for (int c = 0; c < 2; ++c) {
                         float most = -CUDART_INF_F;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (y[nt][h][2 * e + c] != -CUDART_INF_F)
-                                    most = fmaxf(most, sc[nt][h][2 * e + c] * (st[h][e] * factor[nt][c]));
+                        for (int i = c; i < 8; i += 2)
+                            if (y[nt][i] != -CUDART_INF_F) most = fmaxf(most, sc[nt][i >> 2][i & 3] * (st[i >> 1] * factor[nt][c]));
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
                         most = fmaxf(most - kOff<BF16>, ref[nt][c]);
@@ -599,43 +578,40 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             }
             // weights, times the values' steps, as the right operand
             uint32_t pf[NT][NP][2][2];
+            float vr[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 4; ++i) vr[i] = __shfl_sync(0xffffffffu, vrel, 8 * i + rk);
+            float w[NT][8];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float vr = __shfl_sync(0xffffffffu, vrel, 16 * h + 8 * e + rk);
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float w[2];
+                for (int i = 0; i < 8; ++i) {
+                    w[nt][i] = ex2(y[nt][i]);
+                    l[nt][i & 1] += w[nt][i];
+                    w[nt][i] *= vr[i >> 1];
+                }
+            if (edge) {  // a hidden position's step may be anything
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float x = ex2(y[nt][h][2 * e + c]);
-                            l[nt][c] += x;
-                            w[c] = x * vr;
-                            if (edge && y[nt][h][2 * e + c] == -CUDART_INF_F) w[c] = 0.0f;  // whatever the step
-                        }
-                        const uint32_t hi2 = pack2(w[0], w[1]);
-                        pf[nt][0][h][e] = transpose8(hi2);
-                        if constexpr (!BF16) {
-                            const float2 f2 = __half22float2(as_h2(hi2));
-                            pf[nt][NP - 1][h][e] = transpose8(pack2(w[0] - f2.x, w[1] - f2.y));
-                        }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (y[nt][i] == -CUDART_INF_F) w[nt][i] = 0.0f;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t hi2 = pack2(w[nt][2 * i], w[nt][2 * i + 1]);
+                    pf[nt][0][i >> 1][i & 1] = transpose8(hi2);
+                    if constexpr (!BF16) {
+                        const float2 f2 = __half22float2(as_h2(hi2));
+                        pf[nt][NP - 1][i >> 1][i & 1] = transpose8(pack2(w[nt][2 * i] - f2.x, w[nt][2 * i + 1] - f2.y));
                     }
                 }
             // O = O + V^T P
-            float eight[NT][4];
-            if constexpr (!VEX) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    eight[nt][0] = eight[nt][1] = eight[nt][2] = eight[nt][3] = 0.0f;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        mma_f16(eight[nt], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, pf[nt][0][h][0], pf[nt][0][h][1]);
-                }
-            }
             uint32_t vw[8][VW];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) take<D / 16>(slot_out + Ring<D>::value(i), vw[i]);
+            for (int i = 0; i < 8; ++i) take<D / 16>(slot_out + Ring<D>::value(i), lane, vw[i]);
 #pragma unroll
             for (int j = 0; j < VW; ++j)
 #pragma unroll
@@ -645,20 +621,23 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            halves<VEX>(__byte_perm(vw[4 * h + 2 * e][j], vw[4 * h + 2 * e + 1][j], u ? 0x7632 : 0x5410), x[h][e]);
+                            halves(__byte_perm(vw[4 * h + 2 * e][j], vw[4 * h + 2 * e + 1][j], u ? 0x7632 : 0x5410), magic, x[h][e]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int odd = 0; odd < 2; ++odd) {
                             float acc[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[i] = VEX ? 0.0f : eight[nt][i] * (odd ? 16.0f : 1.0f);
-#pragma unroll
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int k2 = NP - 1; k2 >= 0; --k2)
-                                    mma_f16(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2], pf[nt][k2][h][0],
-                                            pf[nt][k2][h][1]);
+                                for (int k2 = NP - 1; k2 >= 0; --k2) {
+                                    if (h == 0 && k2 == NP - 1)
+                                        mma_f16_first(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2],
+                                                      pf[nt][k2][h][0], pf[nt][k2][h][1]);
+                                    else
+                                        mma_f16(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2], pf[nt][k2][h][0],
+                                                pf[nt][k2][h][1]);
+                                }
                             float(&dst)[4] = o[nt][4 * j + 2 * u + odd];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) dst[i] = fmaf(vtop, acc[i], dst[i]);
@@ -680,10 +659,9 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 if (g == 0) sm[warp][n] = ref[nt][c], sl[warp][n] = l[nt][c];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const float f = VEX ? 1.0f : ((i & 1) ? 0x1p20f : 0x1p24f);
                     const int d = g * (D / 8) + 8 * (i >> 2) + 4 * ((i >> 1) & 1) + (i & 1);
-                    so[(warp * R + n) * LD + d] = o[nt][i][c] * f;
-                    so[(warp * R + n) * LD + d + 2] = o[nt][i][2 + c] * f;
+                    so[(warp * R + n) * LD + d] = o[nt][i][c];
+                    so[(warp * R + n) * LD + d + 2] = o[nt][i][2 + c];
                 }
             }
         __syncthreads();
@@ -843,6 +821,7 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
     p.window = window > 0 && window < INT32_MAX ? (int)window : INT32_MAX;
     p.rows_max = INT32_MAX;
     p.out = out, p.lse = lse, p.status = device_status_ptr();
+    p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
     const int64_t rows = (max_q > 0 ? max_q : T) * p.group;
     const bool two = rows > 8;
     if (c.dim == 64) {
