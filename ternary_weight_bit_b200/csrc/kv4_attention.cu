@@ -22,6 +22,7 @@ constexpr uint32_t kNowhere = 0xffffffffu;
 constexpr int kTile = 32;       // positions that a warp takes at a time
 constexpr int kMaxParts = 64;   // CTAs that may share an item on average
 constexpr int kMinTiles = 4;    // tiles that make a CTA of its own worth while
+constexpr int kItemCost = 10;   // what beginning and ending an item takes, in tiles
 // Weights are held as 2^(s - m + kOff), and a score may pass the running maximum m by kLag before
 // that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
 // for a finer second part.
@@ -32,6 +33,18 @@ constexpr float kLag = BF16 ? 8.0f : 1.0f;
 constexpr float kNone = -3.0e38f;  // reference (m - kOff) of a row that has seen nothing yet
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+template <int N>
+struct Const {
+    __host__ __device__ constexpr operator int() const { return N; }
+};
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {  // f(constant 0), ..., f(constant N - 1)
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(Const<N - 1>());
+    }
+}
 
 // A stage of a warp's ring: a tile's codes and steps, each lane's 16 (8, 4) bytes beside the others'.
 template <int D>
@@ -62,7 +75,6 @@ struct RowsParams {
     int causal;
     int window;   // INT32_MAX: none
     int rows_max; // sequences with more rows (new tokens x group) are another kernel's
-    int whole;    // 1: items are not split
     void *out;
     float *lse;
     float *part;  // [grid][2][8 NT][D + 2]: output, reference, sum
@@ -119,40 +131,34 @@ __device__ __forceinline__ void halves(uint32_t w, const uint32_t (&magic)[2], u
     h[3] = h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth, off16));
 }
 
-// A lane's copy of BYTES (4, 8 or a multiple of 16) into its own place in shared memory, where dst is the
-// warp's; zeros where !on (nothing is read then).
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int lane, bool on) {
-    constexpr int N = BYTES < 16 ? BYTES : 16;
-#pragma unroll
-    for (int i = 0; i < BYTES / N; ++i) {
-        const uint32_t to = dst + lane * N + i * 512;
-        const char *from = reinterpret_cast<const char *>(src) + 16 * i;
-        if constexpr (N == 16)
-            asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.cg.shared.global [%0], [%1], 16, p;}" ::"r"(to), "l"(from),
-                         "r"((uint32_t)on)
-                         : "memory");
-        else
-            asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.ca.shared.global [%0], [%1], %3, p;}" ::"r"(to), "l"(from),
-                         "r"((uint32_t)on), "n"(N)
-                         : "memory");
+// A lane's copy of BYTES (4, 8 or a multiple of 16) into its own place in shared memory, dst + TO; zeros where
+// !on (nothing is read then).  Lanes stand min(BYTES, 16) apart, and each 16 bytes have a plane of their own.
+template <int BYTES, int TO, int FROM>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t on) {
+    if constexpr (BYTES >= 16) {
+        asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, p;}" ::"r"(dst),
+                     "l"(src), "r"(on), "n"(TO), "n"(FROM)
+                     : "memory");
+        if constexpr (BYTES > 16) copy_async<BYTES - 16, TO + 512, FROM + 16>(dst, src, on);
+    } else {
+        asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.ca.shared.global [%0 + %3], [%1 + %4], %5, p;}" ::"r"(dst),
+                     "l"(src), "r"(on), "n"(TO), "n"(FROM), "n"(BYTES)
+                     : "memory");
     }
 }
-// What copy_async<BYTES> put there.
-template <int BYTES>
-__device__ __forceinline__ void take(uint32_t src, int lane, uint32_t (&w)[BYTES / 4]) {
-    src += lane * (BYTES < 16 ? BYTES : 16);
+// What copy_async<BYTES, FROM, .> put there.
+template <int BYTES, int FROM>
+__device__ __forceinline__ void take(uint32_t src, uint32_t *w) {
     if constexpr (BYTES == 4) {
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(src) : "memory");
+        asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(src), "n"(FROM) : "memory");
     } else if constexpr (BYTES == 8) {
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(w[0]), "=r"(w[1]) : "r"(src), "n"(FROM) : "memory");
     } else {
-#pragma unroll
-        for (int i = 0; i < BYTES / 16; ++i)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
-                         : "r"(src + i * 512)
-                         : "memory");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(src), "n"(FROM)
+                     : "memory");
+        if constexpr (BYTES > 16) take<BYTES - 16, FROM + 512>(src, w + 4);
     }
 }
 template <int N>
@@ -187,7 +193,7 @@ __device__ __forceinline__ Seq seq_of(const RowsParams &p, int b) {
     return s;
 }
 __device__ __forceinline__ int64_t weight(const RowsParams &p, const Seq &s) {
-    return (int64_t)s.row_tiles * p.c.heads * (p.whole ? 1 : s.tiles);
+    return (int64_t)s.row_tiles * p.c.heads * (s.tiles + kItemCost);
 }
 
 // Every CTA takes an equal run of all tiles of all items, in order; the run's first and last
@@ -259,11 +265,11 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         items += scan[kWarps + w];
     }
     int64_t G = gridDim.x;
-    if (!p.whole) G = max((int64_t)1, min(min(G, items * kMaxParts), (W + kMinTiles - 1) / kMinTiles));
+    G = max((int64_t)1, min(min(G, items * kMaxParts), (W + kMinTiles - 1) / kMinTiles));
     const int64_t cta = blockIdx.x;
     const int64_t run0 = cta < G ? W * cta / G : W, run_end = cta < G ? W * (cta + 1) / G : W;
     if (run0 >= run_end) {
-        if (!p.whole && tid == 0) p.head[cta] = make_int4(0, 0, 0, 0);
+        if (tid == 0) p.head[cta] = make_int4(0, 0, 0, 0);
         return;
     }
     if (run0 >= before && run0 < before + mine) {
@@ -289,19 +295,18 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             off -= weight(p, s);
             s = seq_of<R>(p, ++b);
         }
-        const int unit = p.whole ? 1 : s.tiles;
+        const int unit = s.tiles + kItemCost;
         const int item = (int)(off / unit);  // key head * row tiles + row tile
         const int kh = item / s.row_tiles, rt = item - kh * s.row_tiles;
-        const int lo = p.whole ? 0 : (int)(off - (int64_t)item * unit);
-        const int hi = p.whole ? s.tiles : (int)min((int64_t)s.tiles, lo + (run_end - run));
-        const bool whole = lo == 0 && hi == s.tiles;
-        if (!p.whole && run == run0 && tid == 0) {
+        const int from = (int)(off - (int64_t)item * unit), to = (int)min((int64_t)unit, from + (run_end - run));
+        const bool starts = from == 0, whole = starts && to == unit;
+        const int lo = max(0, from - kItemCost), hi = max(0, to - kItemCost);  // tiles
+        if (run == run0 && tid == 0) {
             // where this CTA's first part is the second of its item, it names the CTAs that share the item
             int4 h = make_int4(0, 0, 0, 0);
-            const int64_t first = run0 - lo;  // of the item
-            if (lo > 0 && W * (cta - 1) / G <= first) {
-                int64_t last = cta;
-                while (W * (last + 1) / G < first + s.tiles) ++last;
+            const int64_t first = run0 - from;  // of the item
+            if (!starts && W * (cta - 1) / G <= first) {
+                const int64_t last = ((first + unit) * G + W - 1) / W - 1;  // the first whose run ends behind the item
                 h = make_int4(b, item, (int)(last - cta + 2), 1);
             }
             p.head[cta] = h;
@@ -316,42 +321,108 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         const int all_begin = p.causal ? (int)max((int64_t)0, (int64_t)base + tok1 - p.window + 1) : 0;
         const int tile0 = begin / kTile;
         // position 0 is kept at 8 bits: the item's first warp begins with it, and no tile has it
-        const int bos_page = lo == 0 && warp == 0 && begin == 0 && end > 0 ? kv4_page(p.c, p.bt, b, 0, p.status) : -1;
+        const int bos_page = starts && warp == 0 && begin == 0 && end > 0 ? kv4_page(p.c, p.bt, b, 0, p.status) : -1;
 
+        // The warp's tiles lo + warp, + kWarps, ...: their blocks of 16 positions lie in the cache from these
+        // rows on, or kNowhere where no page holds them or nothing in them is seen.  Lane 2 i + h has half h
+        // of tile 16 n + i; the next 16 tiles' page numbers are on their way meanwhile.
+        const uint32_t mask = (1u << p.c.page_log2) - 1;
+        const int count = max(0, (min(hi, (end - tile0 * kTile + kTile - 1) / kTile) - lo - warp + kWarps - 1) / kWarps);
+        auto block_at = [&](int i) { return (tile0 + lo + warp + (i + (lane >> 1)) * kWarps) * kTile + 16 * (lane & 1); };
+        auto wanted = [&](int i) {
+            const int at = block_at(i);
+            return i + (lane >> 1) < count && at < end && at + 16 > begin;
+        };
+        auto page_of = [&](int i) {
+            const int n = block_at(i) >> p.c.page_log2;
+            return wanted(i) && n < p.bt.max_pages ? __ldg(p.bt.table + (int64_t)b * p.bt.table_stride + n) : -1;
+        };
+        auto rows_of = [&](int i, int page) {
+            if (!wanted(i)) return kNowhere;
+            if ((unsigned)page >= (unsigned)p.c.pages) {
+                record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
+                return kNowhere;
+            }
+            return (((uint32_t)page * p.c.heads + kh) << p.c.page_log2) + (block_at(i) & mask);
+        };
+        const int page0 = page_of(0);
+        int pages = page_of(16);
+        // the queries are on their way with the page numbers
+        constexpr int QV = D / 4 / (BF16 ? 8 : 4);
+        uint4 raw[NT][QV];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = row0 + 8 * nt + g, tok = r / p.group;
+            const bool on = 8 * nt + g < nrows;
+            const int64_t at = on ? (int64_t)(q0 + tok) * p.qts + (int64_t)(kh * p.group + r - tok * p.group) * p.qhs + t * (D / 4) : 0;
+            const uint4 *const src = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p.q) + at * (BF16 ? 2 : 4));
+#pragma unroll
+            for (int i = 0; i < QV; ++i) raw[nt][i] = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        }
+        uint32_t rows = rows_of(0, page0);
+
+        const int rk = 4 * (g & 1) + (g >> 1);
+        const uint8_t *const k_base = p.c.k_codes + rk * (D / 2) + t * (D / 8);
+        const uint8_t *const v_base = p.c.v_codes + t * (D / 2) + g * (D / 16);
+        uint32_t valid = 0;  // two bits for each tile under way: whether its blocks lie somewhere
+        auto fetch = [&](int i, uint32_t slot) {  // the copies of the warp's tile i; one group, empty past the end
+            valid <<= 2;
+            if (i < count) {
+                if ((i & 15) == 0 && i > 0) {
+                    rows = rows_of(i, pages);
+                    pages = page_of(i + 16);
+                }
+                uint32_t r[2];
+                const uint32_t to_k = slot + lane * min(D / 8, 16), to_v = slot + lane * min(D / 16, 16);
+                each<2>([&](auto h) {
+                    r[h] = __shfl_sync(0xffffffffu, rows, 2 * (i & 15) + h);
+                    const uint32_t on = r[h] != kNowhere;
+                    valid |= on << h;
+                    const uint64_t off = (uint64_t)(on ? r[h] : 0) * (D / 2);
+                    const uint8_t *const k = k_base + off, *const v = v_base + off;
+                    each<2>([&](auto e) { copy_async<D / 8, Ring<D>::key(2 * h + e), e * 8 * (D / 2)>(to_k, k, on); });
+                    each<4>([&](auto e) { copy_async<D / 16, Ring<D>::value(4 * h + e), e * 4 * (D / 2)>(to_v, v, on); });
+                });
+                const uint32_t own = lane < 16 ? r[0] : r[1];
+                const uint32_t on = own != kNowhere;
+                const uint32_t at = on ? own + (lane & 15) : 0;
+                copy_async<4, Ring<D>::step(0), 0>(slot + lane * 4, p.c.k_step + at, on);
+                copy_async<4, Ring<D>::step(1), 0>(slot + lane * 4, p.c.v_step + at, on);
+            }
+            copies_commit();
+        };
+        uint32_t slot_in = ring, slot_out = ring;
+        auto advance = [&](uint32_t &slot) {
+            slot += Ring<D>::kStage;
+            if (slot == ring + kStages<D, NT> * Ring<D>::kStage) slot = ring;
+        };
+#pragma unroll
+        for (int i = 0; i < kStages<D, NT> - 1; ++i) {
+            fetch(i, slot_in);
+            advance(slot_in);
+        }
         // queries: row 8 nt + g, dimensions t D/4 ...; factor and reference for the rows 2t, 2t + 1
         uint32_t qf[NT][NP][KW][2][2];
         float factor[NT][2], ref[NT][2];
         int pos[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = row0 + 8 * nt + g;
-            const int tok = r / p.group;
-            const bool on = 8 * nt + g < nrows;
-            float x[D / 4];
-            const int64_t at = on ? (int64_t)(q0 + tok) * p.qts + (int64_t)(kh * p.group + r - tok * p.group) * p.qhs + t * (D / 4) : 0;
-            float top = 0.0f;
+            float x[D / 4], top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 4; i += 8) {
-                if constexpr (BF16) {
-                    const uint4 u = on ? __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + at + i))
-                                       : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int i = 0; i < QV; ++i) {
+                const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[i + 2 * j] = __uint_as_float(w[j] << 16);
-                        x[i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j += 4) {
-                        const float4 u = on ? __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.q) + at + i + j))
-                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        x[i + j] = u.x, x[i + j + 1] = u.y, x[i + j + 2] = u.z, x[i + j + 3] = u.w;
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (BF16) {
+                        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                    } else {
+                        x[4 * i + j] = __uint_as_float(w[j]);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i + j]));
             }
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             float z0 = 0.0f;  // this row's product with position 0
@@ -416,74 +487,6 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             }
         }
 
-        // The warp's tiles lo + warp, + kWarps, ...: their blocks of 16 positions lie in the cache from these
-        // rows on, or kNowhere where no page holds them or nothing in them is seen.  Lane 2 i + h has half h
-        // of tile 16 n + i; the next 16 tiles' page numbers are on their way meanwhile.
-        const uint32_t mask = (1u << p.c.page_log2) - 1;
-        const int count = max(0, (min(hi, (end - tile0 * kTile + kTile - 1) / kTile) - lo - warp + kWarps - 1) / kWarps);
-        auto block_at = [&](int i) { return (tile0 + lo + warp + (i + (lane >> 1)) * kWarps) * kTile + 16 * (lane & 1); };
-        auto wanted = [&](int i) {
-            const int at = block_at(i);
-            return i + (lane >> 1) < count && at < end && at + 16 > begin;
-        };
-        auto page_of = [&](int i) {
-            const int n = block_at(i) >> p.c.page_log2;
-            return wanted(i) && n < p.bt.max_pages ? __ldg(p.bt.table + (int64_t)b * p.bt.table_stride + n) : -1;
-        };
-        auto rows_of = [&](int i, int page) {
-            if (!wanted(i)) return kNowhere;
-            if ((unsigned)page >= (unsigned)p.c.pages) {
-                record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
-                return kNowhere;
-            }
-            return (((uint32_t)page * p.c.heads + kh) << p.c.page_log2) + (block_at(i) & mask);
-        };
-        uint32_t rows = rows_of(0, page_of(0));
-        int pages = page_of(16);
-
-        const int rk = 4 * (g & 1) + (g >> 1);
-        const uint8_t *const k_base = p.c.k_codes + rk * (D / 2) + t * (D / 8);
-        const uint8_t *const v_base = p.c.v_codes + t * (D / 2) + g * (D / 16);
-        uint32_t valid = 0;  // two bits for each tile under way: whether its blocks lie somewhere
-        auto fetch = [&](int i, uint32_t slot) {  // the copies of the warp's tile i; one group, empty past the end
-            valid <<= 2;
-            if (i < count) {
-                if ((i & 15) == 0 && i > 0) {
-                    rows = rows_of(i, pages);
-                    pages = page_of(i + 16);
-                }
-                uint32_t r[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    r[h] = __shfl_sync(0xffffffffu, rows, 2 * (i & 15) + h);
-                    const bool on = r[h] != kNowhere;
-                    valid |= on << h;
-                    const uint64_t off = (uint64_t)(on ? r[h] : 0) * (D / 2);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        copy_async<D / 8>(slot + Ring<D>::key(2 * h + e), k_base + off + e * 8 * (D / 2), lane, on);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        copy_async<D / 16>(slot + Ring<D>::value(4 * h + e), v_base + off + e * 4 * (D / 2), lane, on);
-                }
-                const uint32_t own = lane < 16 ? r[0] : r[1];
-                const bool on = own != kNowhere;
-                const uint32_t at = on ? own + (lane & 15) : 0;
-                copy_async<4>(slot + Ring<D>::step(0), p.c.k_step + at, lane, on);
-                copy_async<4>(slot + Ring<D>::step(1), p.c.v_step + at, lane, on);
-            }
-            copies_commit();
-        };
-        uint32_t slot_in = ring, slot_out = ring;
-        auto advance = [&](uint32_t &slot) {
-            slot += Ring<D>::kStage;
-            if (slot == ring + kStages<D, NT> * Ring<D>::kStage) slot = ring;
-        };
-#pragma unroll
-        for (int i = 0; i < kStages<D, NT> - 1; ++i) {
-            fetch(i, slot_in);
-            advance(slot_in);
-        }
         for (int it = 0; it < count; ++it) {
             const int at = (tile0 + lo + warp + it * kWarps) * kTile;
             fetch(it + kStages<D, NT> - 1, slot_in);
@@ -492,11 +495,11 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
 
             // S = K Q^T
             float sc[NT][2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            const uint32_t from_k = slot_out + lane * min(D / 8, 16), from_v = slot_out + lane * min(D / 16, 16);
+            each<2>([&](auto h) {
                 uint32_t kw[2][KW];
-                take<D / 8>(slot_out + Ring<D>::key(2 * h), lane, kw[0]);
-                take<D / 8>(slot_out + Ring<D>::key(2 * h + 1), lane, kw[1]);
+                take<D / 8, Ring<D>::key(2 * h)>(from_k, kw[0]);
+                take<D / 8, Ring<D>::key(2 * h + 1)>(from_k, kw[1]);
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     uint32_t x[4], y[4];
@@ -513,15 +516,15 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                             mma_f16(sc[nt][h], x[1], y[1], x[3], y[3], qf[nt][k2][j][1][0], qf[nt][k2][j][1][1]);
                         }
                 }
-            }
+            });
             // the lane's own position: its key step, and its value step over a power of two that
             // no step of the tile is twice as large as (one that is not finite stays with its position)
             const int own = at + lane;
-            uint32_t steps[2][1];
-            take<4>(slot_out + Ring<D>::step(0), lane, steps[0]);
-            take<4>(slot_out + Ring<D>::step(1), lane, steps[1]);
+            uint32_t steps[2];
+            take<4, Ring<D>::step(0)>(slot_out + lane * 4, &steps[0]);
+            take<4, Ring<D>::step(1)>(slot_out + lane * 4, &steps[1]);
             const bool live = own >= max(begin, 1) && own < end && (valid >> (2 * (kStages<D, NT> - 1) + (lane >> 4)) & 1);
-            const float kstep = live ? __uint_as_float(steps[0][0]) : 0.0f, vstep = live ? __uint_as_float(steps[1][0]) : 0.0f;
+            const float kstep = live ? __uint_as_float(steps[0]) : 0.0f, vstep = live ? __uint_as_float(steps[1]) : 0.0f;
             const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
             const uint32_t vbits = __float_as_uint(vstep) & 0x7f800000u;
             const uint32_t vexp = min(max(__reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u), 0x0d000000u), 0x7e000000u);
@@ -610,8 +613,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 }
             // O = O + V^T P
             uint32_t vw[8][VW];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) take<D / 16>(slot_out + Ring<D>::value(i), lane, vw[i]);
+            each<8>([&](auto i) { take<D / 16, Ring<D>::value(i)>(from_v, vw[i]); });
 #pragma unroll
             for (int j = 0; j < VW; ++j)
 #pragma unroll
@@ -665,7 +667,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 }
             }
         __syncthreads();
-        float *part = p.part + ((cta * 2 + (lo > 0 ? 0 : 1)) * R) * (D + 2);
+        float *part = p.part + ((cta * 2 + (starts ? 1 : 0)) * R) * (D + 2);
         for (int i = tid; i < nrows * (D / 4); i += 32 * kWarps) {
             const int n = i / (D / 4), d = 4 * (i % (D / 4));
             float top = kNone, sum = 0.0f;
@@ -698,9 +700,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             if (p.lse && d == 0) p.lse[at] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
         }
         __syncthreads();
-        const int64_t done = p.whole ? 1 : hi - lo;
-        run += done;
-        off += done;
+        run += to - from;
+        off += to - from;
     }
 }
 
@@ -756,8 +757,6 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
     }
 }
 
-constexpr int kMaxGrid = 4 * 148 * 4;
-
 template <typename... P, typename... A>
 cudaError_t launch_one(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
@@ -792,7 +791,6 @@ cudaError_t launch_rows(RowsParams p, int64_t T, void *ws, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int slots = sm_count() * kResident<D, NT>;
     const int grid = slots;
-    p.whole = 0;
     p.head = static_cast<int4 *>(ws);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + (size_t)grid * sizeof(int4));
     const cudaError_t r = launch_one(kv4_rows_kernel<D, NT, BF16>, grid, 32 * kWarps, smem, s, p);
