@@ -134,6 +134,12 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
                                  const Kv4Cache &c, const Kv4Batch &bt, float scale, bool causal, int64_t window,
                                  int64_t max_q, void *out, float *lse, void *ws, cudaStream_t s);
 
+// Its bf16 calls' sequences of at least rows_min rows (new tokens x query heads of a key head), dim 64 or 128
+// (kv4_prefill.cu).  window: INT32_MAX for none.
+cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts, int64_t qhs, const Kv4Cache &c,
+                             const Kv4Batch &bt, float scale, bool causal, int window, int rows_min, void *out, float *lse,
+                             cudaStream_t s);
+
 // Argument rules shared by every forward entry point (the workspace is checked by
 // each entry point): BITNET_OK or the status the call returns.
 bitnet_status_t validate_forward(const void *X, bitnet_dtype_t xdt, int64_t M, int64_t K, const float *gain,

@@ -31,6 +31,7 @@ constexpr float kOff = BF16 ? 6.0f : 13.0f;
 template <bool BF16>
 constexpr float kLag = BF16 ? 8.0f : 1.0f;
 constexpr float kNone = -3.0e38f;  // reference (m - kOff) of a row that has seen nothing yet
+constexpr int kTilesFrom = 128;  // rows of a sequence from which on kv4_prefill.cu takes them
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -817,10 +818,17 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
     p.q = q, p.qts = qts, p.qhs = qhs, p.q_heads = q_heads, p.group = q_heads / c.heads, p.T = T;
     p.c = c, p.bt = bt, p.scale = scale, p.causal = causal;
     p.window = window > 0 && window < INT32_MAX ? (int)window : INT32_MAX;
-    p.rows_max = INT32_MAX;
+    // Longer runs of rows go to the tcgen05 kernel where there is one.  max_q is a hint: without that kernel
+    // every sequence is this one's.
+    const int64_t rows = (max_q > 0 && max_q < T ? max_q : T) * p.group;
+    const bool tiles = bf16 && c.dim <= 128 && rows >= kTilesFrom;
+    p.rows_max = tiles ? kTilesFrom - 1 : INT32_MAX;
     p.out = out, p.lse = lse, p.status = device_status_ptr();
     p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
-    const int64_t rows = (max_q > 0 ? max_q : T) * p.group;
+    if (tiles) {
+        const cudaError_t e = launch_kv4_tiles(q, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, s);
+        if (e != cudaSuccess) return e;
+    }
     const bool two = rows > 8;
     if (c.dim == 64) {
         if (two) return bf16 ? launch_rows<64, 2, true>(p, T, ws, s) : launch_rows<64, 2, false>(p, T, ws, s);

@@ -1,0 +1,683 @@
+// kv4_prefill.cu -- softmax attention over the 4-bit paged KV cache for many rows (prompts and
+// chunks of prompts), on the tcgen05 tensor cores.
+//
+// Method: bitnet_v2_engine.py page, BitNetV2Attention.forward on the fake-quantised keys and
+// values, as in kv4_attention.cu: s_t = scale * kstep_t * (q . kcode_t),
+// out = sum_t e^(s_t) vstep_t vcode_t / sum_t e^(s_t).
+//
+// A CTA takes 256 rows (new tokens x query heads) that share a key head, as two tiles of 128,
+// and walks their positions 128 at a time:
+//
+//   warps 0-3, 4-7   softmax of tile 0, tile 1: a thread owns a row
+//   warps 8-11       codes -> fp16 in shared memory: a thread owns a position
+//   warp 12          issues the products
+//
+//   S_w = Q_w K^T      both operands in shared memory, K-major, 128-byte swizzle; S in TMEM
+//   P_w                fp16 weights, stored by the softmax warps over the first half of S_w
+//   O_w += P_w V       P from TMEM, V in shared memory with the dimensions contiguous
+//
+// While one tile's softmax runs, the tensor cores work for the other.  The codes are exact in
+// fp16; steps are fp32 factors of the scores' and the weights' columns.  Each group of 8 dimensions
+// stands in shared memory in the order 0 4 1 5 2 6 3 7, as the nibbles come out of a word; queries
+// are stored in the same order and outputs are put back.
+//
+// As in kv4_attention.cu, a row's reference moves only when a score passes it by more than kLag,
+// and value steps are divided by a power of two that no step so far is twice as large as; O is
+// rescaled in TMEM in those rare cases alone.
+#include "kv4.cuh"
+
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+namespace bitnet {
+
+namespace {
+
+constexpr int kRows = 128;   // rows of a tile
+constexpr int kPos = 128;    // positions of a step
+constexpr int kThreads = 512;
+constexpr int kKS = 2, kVS = 2, kStepStages = 4;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;  // registers of a thread; 256 threads each
+constexpr uint32_t kNowhere = 0xffffffffu;
+constexpr float kOff = 6.0f, kLag = 8.0f, kNone = -3.0e38f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct TileParams {
+    const void *q;
+    int64_t qts, qhs;
+    int q_heads, group;
+    int64_t T;
+    Kv4Cache c;
+    Kv4Batch bt;
+    float scale;
+    int causal, window;  // INT32_MAX: none
+    int rows_min;        // sequences with fewer rows are another kernel's
+    uint16_t *out;
+    float *lse;
+    int *status;
+    uint32_t magic[2];  // {0x64086408, 0x64806480}, as data: a logic instruction takes one constant
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kTile = kRows * D * 2;  // bytes of a tile of Q, K or V
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + 2 * kTile;
+    static constexpr int kV = kK + kKS * kTile;
+    static constexpr int kSteps = kV + kVS * kTile;            // [kStepStages][2][128] floats: key steps, value ratios
+    static constexpr int kMeta = kSteps + kStepStages * 1024;  // [kStepStages][8]: 4 words of live positions, the power of two
+    static constexpr int kMax = kMeta + kStepStages * 32;      // [2][4]: the warps' largest value steps
+    static constexpr int kBars = kMax + 32;
+    static constexpr int kNumBars = 2 * kKS + 2 * kVS + kStepStages + 2 + 2 + 3;
+    static constexpr int kSlot = kBars + 8 * kNumBars;
+    static constexpr int kUsed = kSlot + 16 + 1024;  // and alignment
+    static constexpr int kBytes = D == 128 ? 231424 : 160 * 1024;
+    static_assert(kUsed <= kBytes && kBytes <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two floats in one register pair.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(f2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t h2(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A 128-byte-swizzled tile of rows of 64 halves.  K-major (Q, K): a row is 64 of the summed
+// dimension, the next 8 rows lie 1024 bytes on.  Dimensions contiguous (V): a row is one position, the next 8
+// positions lie 1024 bytes on, the next 64 dimensions kRows rows on.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, bool mn) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(mn ? (kRows * 128) >> 4 : 1) << 16;  // leading byte offset: the next 64 dimensions (V); unused (Q, K)
+    d |= (uint64_t)(1024 >> 4) << 32;           // stride byte offset: the next 8 rows
+    d |= (uint64_t)1 << 46;                     // descriptor version (sm100)
+    d |= (uint64_t)2 << 61;                     // swizzle: 128B
+    return d;
+}
+// D = f32, A = B = f16, M = 128.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+// Called by a converged warp; one lane issues.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+}
+
+// Eight codes of a word as 16 bytes of fp16, dimensions in the order 0 4 1 5 2 6 3 7 (see halves() in
+// kv4_attention.cu).
+__device__ __forceinline__ void put_codes(uint32_t dst, uint32_t w, const uint32_t (&magic)[2]) {
+    const uint32_t v = w >> 8;
+    const __half2 off = __float2half2_rn(-1032.0f), off16 = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
+    sts128(dst, h2(__hadd2(as_h2((w & 0x000F000Fu) ^ magic[0]), off)),
+           h2(__hfma2(as_h2((w & 0x00F000F0u) ^ magic[1]), sixteenth, off16)),
+           h2(__hadd2(as_h2((v & 0x000F000Fu) ^ magic[0]), off)),
+           h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth, off16)));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_constant__ TileParams p) {
+    using S = Smem<D>;
+    extern __shared__ char smem_raw[];
+    __shared__ int item_of[4];
+    __shared__ int64_t scan[kThreads / 32];
+
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+
+    // this CTA's 256 rows: the blockIdx-th from the end over all sequences, pairs of tiles and heads
+    const int B = p.bt.batch;
+    const int per = (B + kThreads - 1) / kThreads;
+    auto pairs_of = [&](int b) {
+        const int a = max(0, __ldg(p.bt.starts + b));
+        const int64_t n = min((int64_t)max(0, __ldg(p.bt.starts + b + 1) - a), max((int64_t)0, p.T - a));
+        const int64_t rows = n * p.group;
+        return rows < p.rows_min ? 0 : (int)((rows + 2 * kRows - 1) / (2 * kRows));
+    };
+    int64_t mine = 0;
+    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) mine += pairs_of(b);
+    int64_t before = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, before, x);
+        if (lane >= x) before += y;
+    }
+    if (lane == 31) scan[warp] = before;
+    __syncthreads();
+    int64_t total = 0;
+    before -= mine;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? scan[w] : 0;
+        total += scan[w];
+    }
+    const int64_t index = total * p.c.heads - 1 - blockIdx.x;
+    if (index < 0) return;  // the same for the whole CTA
+    {
+        const int64_t at = index / p.c.heads;
+        if (at >= before && at < before + mine) {
+            int64_t off = at - before;
+            int b = tid * per;
+            while (off >= pairs_of(b)) off -= pairs_of(b++);
+            item_of[0] = b;
+            item_of[1] = (int)off;
+            item_of[2] = (int)(index % p.c.heads);
+        }
+    }
+    const uint32_t bars = base + S::kBars;
+    const uint32_t k_full = bars, k_empty = k_full + 8 * kKS, v_full = k_empty + 8 * kKS, v_empty = v_full + 8 * kVS,
+                   st_full = v_empty + 8 * kVS, s_full = st_full + 8 * kStepStages, p_full = s_full + 16, q_full = p_full + 16,
+                   o_full = q_full + 8, mx_full = o_full + 8;
+    if (tid == 0) {
+        auto init = [&](uint32_t bar, int n) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+        };
+        for (int i = 0; i < kKS; ++i) init(k_full + 8 * i, 128), init(k_empty + 8 * i, 1);
+        for (int i = 0; i < kVS; ++i) init(v_full + 8 * i, 128), init(v_empty + 8 * i, 1);
+        for (int i = 0; i < kStepStages; ++i) init(st_full + 8 * i, 128);
+        for (int w = 0; w < 2; ++w) init(s_full + 8 * w, 1), init(p_full + 8 * w, 128);
+        init(q_full, 256);
+        init(o_full, 1);
+        init(mx_full, 128);
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + S::kSlot), "r"(512) : "memory");
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lds32(base + S::kSlot);
+    const int b = item_of[0], kh = item_of[2];
+
+    const int first = max(0, __ldg(p.bt.starts + b));
+    const int n = max(0, __ldg(p.bt.starts + b + 1) - first);
+    const int len = max(0, __ldg(p.bt.lens + b));
+    const int pos0 = len - n;  // of the sequence's first row
+    const int cap = (int)min((int64_t)len, (int64_t)p.bt.max_pages << p.c.page_log2);
+    const int rows = (int)(min((int64_t)n, p.T - first) * p.group);
+    const int row0 = item_of[1] * 2 * kRows;
+    const int row_last = min(row0 + 2 * kRows, rows) - 1;
+    const int end = p.causal ? min(cap, pos0 + row_last / p.group + 1) : cap;
+    const int begin = p.causal ? (int)max((int64_t)0, (int64_t)pos0 + row0 / p.group - p.window + 1) : 0;
+    const int step0 = begin / kPos;
+    const int steps = max(0, (end - step0 * kPos + kPos - 1) / kPos);
+    if (tid == 0 && cap < len) record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int w = warp >> 2;
+        const int r = tid & 127;                     // row of the tile, and lane of TMEM
+        const int row = row0 + w * kRows + r;        // row of the sequence
+        const bool on = row < rows;
+        const int tok = row / p.group;
+        const int64_t at = on ? (int64_t)(first + tok) * p.q_heads + kh * p.group + (row - tok * p.group) : 0;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_off + w * kPos, t_o = tmem + lane_off + 2 * kPos + w * D;
+
+        // the query: scaled by a power of two into [2^14, 2^15), fp16, and the sign of the scale with it
+        float f;
+        {
+            const int64_t src = on ? (int64_t)(first + tok) * p.qts + (int64_t)(kh * p.group + (row - tok * p.group)) * p.qhs : 0;
+            const uint4 *const q = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + src);
+            uint4 raw[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) raw[i] = on ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+            uint32_t top = 0;
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    top = max(top, max((x[j] << 16) & 0x7fffffffu, x[j] & 0x7fff0000u));
+                }
+            }
+            bad = top > 0x7f800000u;  // a NaN: the row's other values do not matter
+            const uint32_t up_bits = min(max(0x86000000u - (top & 0x7f800000u), 0x07800000u), 0x7e800000u);
+            const float up = top > 0 && !bad ? __uint_as_float(up_bits) : 1.0f;
+            const float sup = p.scale < 0.0f ? -up : up;
+            f = fmaxf(fabsf(p.scale) * kLog2e * (1.0f / up), 1.0e-37f);
+            const uint32_t dst = base + S::kQ + w * S::kTile + r * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y[2 * j] = __uint_as_float(x[j] << 16) * sup;
+                    y[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u) * sup;
+                }
+                sts128(dst + (i >> 3) * (kRows * 128) + (((i & 7) ^ (r & 7)) << 4), pack2(y[0], y[4]), pack2(y[1], y[5]),
+                       pack2(y[2], y[6]), pack2(y[3], y[7]));
+            }
+            fence_proxy_async_smem();
+            arrive(q_full);
+        }
+
+        // positions that this row sees, and those that all rows of the tile see
+        const int tile_first = (row0 + w * kRows) / p.group, tile_last = min(row0 + (w + 1) * kRows, rows) - 1;
+        const int my_end = p.causal && on ? pos0 + tok + 1 : INT32_MAX;
+        const int my_begin = p.causal && on ? (int)max((int64_t)0, (int64_t)pos0 + tok - p.window + 1) : 0;
+        const int all_end = p.causal ? min(cap, pos0 + tile_first + 1) : cap;
+        const int all_begin = p.causal ? (int)max((int64_t)0, (int64_t)pos0 + tile_last / p.group - p.window + 1) : 0;
+
+        float ref = kNone;
+        f2 l2 = pair(0.0f, 0.0f);
+        uint32_t vexp = 0x3f800000u;
+        bool ok = true;
+        for (int j = 0; j < steps; ++j) {
+            const int at0 = (step0 + j) * kPos;
+            const int st = j % kStepStages;
+            if (!mbar_wait_warp(s_full + 8 * w, j & 1, p.status) || !mbar_wait_warp(st_full + 8 * st, (j / kStepStages) & 1, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t steps_at = base + S::kSteps + st * 1024, meta = base + S::kMeta + st * 32;
+            float s[kPos];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+            const uint32_t live[4] = {lds32(meta), lds32(meta + 4), lds32(meta + 8), lds32(meta + 12)};
+            const uint32_t vexp_new = lds32(meta + 16);
+            tmem_wait_ld();
+            f2 z[kPos / 2];
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int i = 0; i < kPos / 4; ++i) {
+                const float4 k = lds_f4(steps_at + 16 * i);
+                z[2 * i] = mul2(pair(s[4 * i], s[4 * i + 1]), pair(k.x, k.y));
+                z[2 * i + 1] = mul2(pair(s[4 * i + 2], s[4 * i + 3]), pair(k.z, k.w));
+            }
+            const bool edge = at0 < all_begin || at0 + kPos > all_end || (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
+            if (edge) {
+                const int lo = my_begin - at0, hi = my_end - at0;  // bits lo .. hi - 1
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int a = min(max(lo - 32 * c, 0), 32), e = min(max(hi - 32 * c, 0), 32);
+                    uint32_t m = live[c];
+                    m &= e >= 32 ? 0xffffffffu : (1u << e) - 1u;
+                    m &= a >= 32 ? 0u : ~((1u << a) - 1u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x, y;
+                        split(z[16 * c + i], x, y);
+                        x = (m >> (2 * i) & 1) ? x : -CUDART_INF_F;
+                        y = (m >> (2 * i + 1) & 1) ? y : -CUDART_INF_F;
+                        z[16 * c + i] = pair(x, y);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPos / 2; ++i) {
+                float x, y;
+                split(z[i], x, y);
+                top = fmaxf(top, fmaxf(x, y));
+            }
+            const bool over = fmaf(top, f, -ref) > kOff + kLag;
+            if (__any_sync(0xffffffffu, over) || vexp_new != vexp) {
+                const float next = over ? fmaf(top, f, -kOff) : ref;
+                const float a = ex2(ref - next);
+                ref = next;
+                l2 = mul2(l2, pair(a, a));
+                if (j > 0) {
+                    // vexp / vexp_new, both powers of two
+                    const float scale = a * __uint_as_float(vexp) * __uint_as_float(0x7f000000u - vexp_new);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(t_o + 32 * c, o);
+                        tmem_wait_ld();
+                        uint32_t lo16[16], hi16[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            lo16[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
+                            hi16[i] = __float_as_uint(__uint_as_float(o[16 + i]) * scale);
+                        }
+                        tmem_st_x16(t_o + 32 * c, lo16);
+                        tmem_st_x16(t_o + 32 * c + 16, hi16);
+                    }
+                }
+                vexp = vexp_new;
+            }
+            const f2 ff = pair(f, f), nref = pair(-ref, -ref);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t h[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 v = lds_f4(steps_at + 512 + 128 * c + 16 * i);
+                    float x[4];
+                    split(fma2(z[16 * c + 2 * i], ff, nref), x[0], x[1]);
+                    split(fma2(z[16 * c + 2 * i + 1], ff, nref), x[2], x[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+                    f2 w0 = pair(x[0], x[1]), w1 = pair(x[2], x[3]);
+                    l2 = add2(l2, w0);
+                    l2 = add2(l2, w1);
+                    w0 = mul2(w0, pair(v.x, v.y));
+                    w1 = mul2(w1, pair(v.z, v.w));
+                    split(w0, x[0], x[1]);
+                    split(w1, x[2], x[3]);
+                    if (edge) {  // a hidden position's step may be anything
+                        float y[4];
+                        split(z[16 * c + 2 * i], y[0], y[1]);
+                        split(z[16 * c + 2 * i + 1], y[2], y[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = y[e] == -CUDART_INF_F ? 0.0f : x[e];
+                    }
+                    h[2 * i] = pack2(x[0], x[1]);
+                    h[2 * i + 1] = pack2(x[2], x[3]);
+                }
+                tmem_st_x16(t_s + 16 * c, h);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(p_full + 8 * w);
+        }
+        // the outputs
+        float l0, l1;
+        split(l2, l0, l1);
+        const float l = l0 + l1;
+        if (steps > 0 && ok) ok = mbar_wait_warp(o_full, 0, p.status);
+        tc_fence_after();
+        if (ok) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (steps > 0) {
+                    tmem_ld_32x32b_x32(t_o + 32 * c, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                if (on) {
+                    uint4 *const dst = reinterpret_cast<uint4 *>(p.out + at * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * i + e]) * __uint_as_float(vexp) * inv;
+                        dst[i] = make_uint4(bf2(y[0], y[2]), bf2(y[4], y[6]), bf2(y[1], y[3]), bf2(y[5], y[7]));
+                    }
+                }
+            }
+            if (on && p.lse) p.lse[at] = l == 0.0f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp < 12) {
+            // ------------------------------------------------------------ codes -> fp16
+            const int i = tid - 256;  // position within the step
+            const uint32_t magic[2] = {p.magic[0], p.magic[1]};
+            const uint32_t mask = (1u << p.c.page_log2) - 1;
+            auto wanted = [&](int j) {
+                const int pos = (step0 + j) * kPos + i;
+                return j < steps && pos < end && pos >= begin;
+            };
+            auto page_of = [&](int j) {
+                const int at = ((step0 + j) * kPos + i) >> p.c.page_log2;
+                return wanted(j) && at < p.bt.max_pages ? __ldg(p.bt.table + (int64_t)b * p.bt.table_stride + at) : -1;
+            };
+            auto row_of = [&](int j, int page) {
+                if (!wanted(j)) return kNowhere;
+                if ((unsigned)page >= (unsigned)p.c.pages) {
+                    record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
+                    return kNowhere;
+                }
+                return (((uint32_t)page * p.c.heads + kh) << p.c.page_log2) + (((step0 + j) * kPos + i) & mask);
+            };
+            uint4 kc[D / 32], vc[D / 32];
+            float ks = 0.0f, vs = 0.0f;
+            auto load_keys = [&](uint32_t r) {
+                const uint4 *const src = reinterpret_cast<const uint4 *>(p.c.k_codes + (uint64_t)(r == kNowhere ? 0 : r) * (D / 2));
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) kc[c] = r != kNowhere ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                ks = r != kNowhere ? __ldg(p.c.k_step + r) : 0.0f;
+                vs = r != kNowhere ? __ldg(p.c.v_step + r) : 0.0f;
+            };
+            auto load_values = [&](uint32_t r) {
+                const uint4 *const src = reinterpret_cast<const uint4 *>(p.c.v_codes + (uint64_t)(r == kNowhere ? 0 : r) * (D / 2));
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) vc[c] = r != kNowhere ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            };
+            auto put_row = [&](uint32_t tile, const uint4 (&c)[D / 32]) {
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    const uint32_t x[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int g = 4 * q + e;  // eight dimensions
+                        put_codes(tile + (g >> 3) * (kRows * 128) + i * 128 + (((g & 7) ^ (i & 7)) << 4), x[e], magic);
+                    }
+                }
+            };
+            auto put_bos = [&](uint32_t tile, const int8_t *c8) {  // position 0 is kept at 8 bits
+                for (int g = 0; g < D / 8; ++g) {
+                    const char4 a = *reinterpret_cast<const char4 *>(c8 + 8 * g), c = *reinterpret_cast<const char4 *>(c8 + 8 * g + 4);
+                    sts128(tile + (g >> 3) * (kRows * 128) + i * 128 + (((g & 7) ^ (i & 7)) << 4), pack2(a.x, c.x), pack2(a.y, c.y),
+                           pack2(a.z, c.z), pack2(a.w, c.w));
+                }
+            };
+            uint32_t r = row_of(0, page_of(0));
+            int page = page_of(1);
+            load_keys(r);
+            load_values(r);
+            uint32_t vexp = 0x0d000000u;  // 2^-101
+            for (int j = 0; j < steps; ++j) {
+                const uint32_t next = row_of(j + 1, page);
+                page = page_of(j + 2);
+                const bool live = r != kNowhere, bos = live && (step0 + j) * kPos + i == 0;
+                const int64_t bos_at = bos ? (int64_t)(r >> p.c.page_log2) * D : 0;
+                const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
+                const uint32_t bits = __float_as_uint(vs) & 0x7f800000u;
+                const uint32_t most = __reduce_max_sync(0xffffffffu, live && bits < 0x7f800000u ? bits : 0u);
+                const uint32_t maxes = base + S::kMax + (j & 1) * 16;
+                if (lane == 0) sts32(maxes + 4 * (warp - 8), most);
+                arrive(mx_full);
+                if (!mbar_wait_warp(mx_full, j & 1, p.status)) break;
+                const float4 m4 = lds_f4(maxes);
+                const uint32_t m01 = max(__float_as_uint(m4.x), __float_as_uint(m4.y)), m23 = max(__float_as_uint(m4.z), __float_as_uint(m4.w));
+                vexp = min(max(vexp, max(m01, m23)), 0x7e000000u);
+
+                const int st = j % kStepStages, sk = j % kKS, sv = j % kVS;
+                if (j >= kKS && !mbar_wait_warp(k_empty + 8 * sk, (j / kKS - 1) & 1, p.status)) break;
+                const uint32_t kt = base + S::kK + sk * S::kTile, steps_at = base + S::kSteps + st * 1024;
+                put_row(kt, kc);
+                if (bos) put_bos(kt, p.c.k_bos + bos_at);
+                sts32(steps_at + 4 * i, __float_as_uint(live ? ks : 0.0f));
+                sts32(steps_at + 512 + 4 * i, __float_as_uint(live ? vs * __uint_as_float(0x7f000000u - vexp) : 0.0f));
+                const uint32_t meta = base + S::kMeta + st * 32;
+                if (lane == 0) sts32(meta + 4 * (warp - 8), live_bits);
+                if (i == 0) sts32(meta + 16, vexp);
+                fence_proxy_async_smem();
+                arrive(k_full + 8 * sk);
+                arrive(st_full + 8 * st);
+                load_keys(next);
+
+                if (j >= kVS && !mbar_wait_warp(v_empty + 8 * sv, (j / kVS - 1) & 1, p.status)) break;
+                const uint32_t vt = base + S::kV + sv * S::kTile;
+                put_row(vt, vc);
+                if (bos) put_bos(vt, p.c.v_bos + bos_at);
+                fence_proxy_async_smem();
+                arrive(v_full + 8 * sv);
+                load_values(next);
+                r = next;
+            }
+        } else if (warp == 12 && steps > 0) {
+            // ------------------------------------------------------------ products
+            bool ok = mbar_wait_warp(q_full, 0, p.status);
+            const uint64_t q_desc = smem_desc(base + S::kQ, false), k_desc = smem_desc(base + S::kK, false),
+                           v_desc = smem_desc(base + S::kV, true);
+            constexpr uint32_t id_s = idesc(kPos, false), id_o = idesc(D, true);
+            for (int j = 0; j <= steps && ok; ++j) {
+                const int sk = j % kKS, sv = (j + kVS - 1) % kVS;  // V of step j - 1
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w) {
+                    if (j > 0) {
+                        if (w == 0 && !mbar_wait_warp(v_full + 8 * sv, ((j - 1) / kVS) & 1, p.status)) ok = false;
+                        if (!ok || !mbar_wait_warp(p_full + 8 * w, (j - 1) & 1, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < kPos / 16; ++k)  // 16 positions: 8 columns of P, 16 rows of V
+                            mma_ts(tmem + 2 * kPos + w * D, tmem + w * kPos + 8 * k, v_desc + (uint64_t)((sv * S::kTile + k * 2048) >> 4), id_o,
+                                   (j > 1 || k > 0) ? 1u : 0u);
+                        if (w == 1) umma_commit_elect(v_empty + 8 * sv);
+                    }
+                    if (j < steps) {
+                        if (w == 0 && !mbar_wait_warp(k_full + 8 * sk, (j / kKS) & 1, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = (k >> 2) * (kRows * 128) + (k & 3) * 32;
+                            mma_ss(tmem + w * kPos, q_desc + (uint64_t)((w * S::kTile + off) >> 4), k_desc + (uint64_t)((sk * S::kTile + off) >> 4),
+                                   id_s, k > 0 ? 1u : 0u);
+                        }
+                        umma_commit_elect(s_full + 8 * w);
+                        if (w == 1) umma_commit_elect(k_empty + 8 * sk);
+                    }
+                }
+            }
+            // also after a wait that gave up: everything issued ends before the CTA does
+            umma_commit_elect(o_full);
+            mbar_wait_warp(o_full, 0, p.status);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch_tiles(const TileParams &p, int64_t grid, cudaStream_t s) {
+    static bool allowed[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kMaxDevices || !allowed[dev]) {
+        e = cudaFuncSetAttribute((const void *)kv4_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+        if (e != cudaSuccess) return e;
+        // the softmax warps' registers come out of what the block is launched with
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, (const void *)kv4_tiles_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs * kThreads < 256 * (kSoftmaxRegs + kOtherRegs)) return cudaErrorInvalidConfiguration;
+        if (dev < kMaxDevices) allowed[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<D>::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_tiles_kernel<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts, int64_t qhs, const Kv4Cache &c,
+                             const Kv4Batch &bt, float scale, bool causal, int window, int rows_min, void *out, float *lse,
+                             cudaStream_t s) {
+    TileParams p = {};
+    p.q = q, p.qts = qts, p.qhs = qhs, p.q_heads = q_heads, p.group = q_heads / c.heads, p.T = T;
+    p.c = c, p.bt = bt, p.scale = scale, p.causal = causal, p.window = window, p.rows_min = rows_min;
+    p.out = static_cast<uint16_t *>(out), p.lse = lse, p.status = device_status_ptr();
+    p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
+    // at most one pair of tiles per sequence is not full
+    const int64_t rows = T * p.group;
+    const int64_t pairs = rows / (2 * kRows) + (rows < (int64_t)bt.batch * rows_min ? rows / rows_min : (int64_t)bt.batch);
+    const int64_t grid = pairs * c.heads;
+    if (grid == 0) return cudaSuccess;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return c.dim == 64 ? launch_tiles<64>(p, grid, s) : launch_tiles<128>(p, grid, s);
+}
+
+}  // namespace bitnet
