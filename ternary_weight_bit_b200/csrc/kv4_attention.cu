@@ -27,9 +27,9 @@ constexpr int kItemCost = 10;   // what beginning and ending an item takes, in t
 // that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
 // for a finer second part.
 template <bool BF16>
-constexpr float kOff = BF16 ? 6.0f : 13.0f;
+constexpr float kOff = BF16 ? 3.0f : 13.0f;
 template <bool BF16>
-constexpr float kLag = BF16 ? 8.0f : 1.0f;
+constexpr float kLag = BF16 ? 11.0f : 1.0f;
 constexpr float kNone = -3.0e38f;  // reference (m - kOff) of a row that has seen nothing yet
 constexpr int kTilesFrom = 128;  // rows of a sequence from which on kv4_prefill.cu takes them
 constexpr float kLog2e = 1.4426950408889634f;
@@ -472,7 +472,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float w = ref[nt][c] == kNone ? 0.0f : (BF16 ? 0x1p6f : 0x1p13f);
+                const float w = ref[nt][c] == kNone ? 0.0f : (BF16 ? 0x1p3f : 0x1p13f);
                 l[nt][c] = g == 0 ? w : 0.0f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) o[nt][i][c] = o[nt][i][2 + c] = w == 0.0f ? 0.0f : w * bos_step;
@@ -519,16 +519,18 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 }
             });
             // the lane's own position: its key step, and its value step over a power of two that
-            // no step of the tile is twice as large as (one that is not finite stays with its position)
+            // no step of the tile is twice as large as
             const int own = at + lane;
             uint32_t steps[2];
             take<4, Ring<D>::step(0)>(slot_out + lane * 4, &steps[0]);
             take<4, Ring<D>::step(1)>(slot_out + lane * 4, &steps[1]);
             const bool live = own >= max(begin, 1) && own < end && (valid >> (2 * (kStages<D, NT> - 1) + (lane >> 4)) & 1);
-            const float kstep = live ? __uint_as_float(steps[0]) : 0.0f, vstep = live ? __uint_as_float(steps[1]) : 0.0f;
+            const uint32_t vbits = live ? steps[1] & 0x7f800000u : 0u;
+            const bool bad = vbits == 0x7f800000u;  // a value step that is not finite: NaN for the rows that see it, and for no others
+            const float kstep = bad ? CUDART_NAN_F : (live ? __uint_as_float(steps[0]) : 0.0f);
+            const float vstep = live && !bad ? __uint_as_float(steps[1]) : 0.0f;
             const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
-            const uint32_t vbits = __float_as_uint(vstep) & 0x7f800000u;
-            const uint32_t vexp = min(max(__reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u), 0x0d000000u), 0x7e000000u);
+            const uint32_t vexp = min(max(__reduce_max_sync(0xffffffffu, bad ? 0u : vbits), 0x0d000000u), 0x7e000000u);
             const float vtop = __uint_as_float(vexp);
             const float vrel = vstep * __uint_as_float(0x7f000000u - vexp);
             const bool edge = at < all_begin || at + kTile > all_end || live_bits != 0xffffffffu;
@@ -594,13 +596,6 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                     l[nt][i & 1] += w[nt][i];
                     w[nt][i] *= vr[i >> 1];
                 }
-            if (edge) {  // a hidden position's step may be anything
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (y[nt][i] == -CUDART_INF_F) w[nt][i] = 0.0f;
-            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

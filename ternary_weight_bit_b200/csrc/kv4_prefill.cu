@@ -39,7 +39,7 @@ constexpr int kThreads = 512;
 constexpr int kKS = 2, kVS = 2, kStepStages = 4;
 constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;  // registers of a thread; 256 threads each
 constexpr uint32_t kNowhere = 0xffffffffu;
-constexpr float kOff = 6.0f, kLag = 8.0f, kNone = -3.0e38f;
+constexpr float kOff = 3.0f, kLag = 11.0f, kNone = -3.0e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct TileParams {
@@ -102,6 +102,11 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     f2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+// x = -inf where !seen.  Volatile, so that it stays inside its branch: as selects the masks of all steps
+// were formed, 4 instructions to a score.
+__device__ __forceinline__ void hide_unless(float &x, uint32_t seen) {
+    asm volatile("{.reg .pred p; setp.ne.u32 p, %1, 0; selp.f32 %0, %0, 0fFF800000, p;}" : "+f"(x) : "r"(seen));
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -375,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                     for (int i = 0; i < 16; ++i) {
                         float x, y;
                         split(z[16 * c + i], x, y);
-                        x = (m >> (2 * i) & 1) ? x : -CUDART_INF_F;
-                        y = (m >> (2 * i + 1) & 1) ? y : -CUDART_INF_F;
+                        hide_unless(x, m & (1u << (2 * i)));
+                        hide_unless(y, m & (2u << (2 * i)));
                         z[16 * c + i] = pair(x, y);
                     }
                 }
@@ -432,13 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                     w1 = mul2(w1, pair(v.z, v.w));
                     split(w0, x[0], x[1]);
                     split(w1, x[2], x[3]);
-                    if (edge) {  // a hidden position's step may be anything
-                        float y[4];
-                        split(z[16 * c + 2 * i], y[0], y[1]);
-                        split(z[16 * c + 2 * i + 1], y[2], y[3]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = y[e] == -CUDART_INF_F ? 0.0f : x[e];
-                    }
                     h[2 * i] = pack2(x[0], x[1]);
                     h[2 * i + 1] = pack2(x[2], x[3]);
                 }
@@ -546,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 const int64_t bos_at = bos ? (int64_t)(r >> p.c.page_log2) * D : 0;
                 const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
                 const uint32_t bits = __float_as_uint(vs) & 0x7f800000u;
+                if (bits == 0x7f800000u) vs = 0.0f, ks = CUDART_NAN_F;  // NaN for the rows that see it, and for no others
                 const uint32_t most = __reduce_max_sync(0xffffffffu, live && bits < 0x7f800000u ? bits : 0u);
                 const uint32_t maxes = base + S::kMax + (j & 1) * 16;
                 if (lane == 0) sts32(maxes + 4 * (warp - 8), most);

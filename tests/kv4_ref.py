@@ -90,8 +90,8 @@ def attention_bounds(out, top, mass, dim, length, dtype, largest):
     2 sqrt(length) roundings.  bf16 calls round weights to fp16 (2^-11) and the output to bf16 (2^-8).
 
     Weights far below the row's largest reach the end of fp16's range.  Weights w step / 2^e, with 2^e at most the
-    largest step among 32 neighbours, are held as multiples of 2^-24 where the largest w is at least 2^6 (bf16 calls) or
-    2^13 (fp32 calls, in their second part): each is off by at most 2^-25, so that of the largest by 2^-31 (2^-38),
+    largest step so far, are held as multiples of 2^-24 where the largest w is at least 2^3 (bf16 calls) or
+    2^13 (fp32 calls, in their second part): each is off by at most 2^-25, so that of the largest by 2^-28 (2^-38),
     times 2^e and a code of at most 8 (127 at position 0).  A row with the step 2^e has a code of 1 or
     more, so 2^e is at most the largest |value| of the sequence (`largest`)."""
     score = 2 * U * (2 * math.sqrt(dim) + 8) * top
@@ -99,5 +99,5 @@ def attention_bounds(out, top, mass, dim, length, dtype, largest):
     if dtype == torch.bfloat16:
         rel = rel + 2.0 ** -11
     err = rel[..., None] * mass + out.abs() * (2.0 ** -8 if dtype == torch.bfloat16 else U) + 1e-37
-    err = err + (2.0 ** -31 if dtype == torch.bfloat16 else 2.0 ** -38) * (8 * length + 127) * largest
+    err = err + (2.0 ** -28 if dtype == torch.bfloat16 else 2.0 ** -38) * (8 * length + 127) * largest
     return err, score + (2 * math.sqrt(length) + 32) * U
