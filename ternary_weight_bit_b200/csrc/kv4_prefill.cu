@@ -9,8 +9,9 @@
 // and walks their positions 128 at a time:
 //
 //   warps 0-3, 4-7   softmax of tile 0, tile 1: a thread owns a row
-//   warps 8-11       codes -> fp16 in shared memory: a thread owns a position
+//   warps 8-11       key codes -> fp16 in shared memory, a thread to a position; places and steps
 //   warp 12          issues the products
+//   warps 13-15      value codes -> fp16
 //
 //   S_w = Q_w K^T      both operands in shared memory, K-major, 128-byte swizzle; S in TMEM
 //   P_w                fp16 weights, stored by the softmax warps over the first half of S_w
@@ -36,7 +37,8 @@ namespace {
 constexpr int kRows = 128;   // rows of a tile
 constexpr int kPos = 128;    // positions of a step
 constexpr int kThreads = 512;
-constexpr int kKS = 2, kVS = 2, kStepStages = 4;
+constexpr int kValueThreads = 96;
+constexpr int kKS = 2, kVS = 2, kStepStages = 4, kPlaceStages = 8;
 constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;  // registers of a thread; 256 threads each
 constexpr uint32_t kNowhere = 0xffffffffu;
 constexpr float kOff = 3.0f, kLag = 11.0f, kNone = -3.0e38f;
@@ -66,9 +68,9 @@ struct Smem {
     static constexpr int kV = kK + kKS * kTile;
     static constexpr int kSteps = kV + kVS * kTile;            // [kStepStages][2][128] floats: key steps, value ratios
     static constexpr int kMeta = kSteps + kStepStages * 1024;  // [kStepStages][8]: 4 words of live positions, the power of two
-    static constexpr int kMax = kMeta + kStepStages * 32;      // [2][4]: the warps' largest value steps
-    static constexpr int kBars = kMax + 32;
-    static constexpr int kNumBars = 2 * kKS + 2 * kVS + kStepStages + 2 + 2 + 3;
+    static constexpr int kPlaces = kMeta + kStepStages * 32;   // [kPlaceStages][128]: the positions' rows in the cache
+    static constexpr int kBars = kPlaces + kPlaceStages * 512;
+    static constexpr int kNumBars = 2 * kKS + 2 * kVS + kStepStages + kPlaceStages + 2 + 2 + 2;
     static constexpr int kSlot = kBars + 8 * kNumBars;
     static constexpr int kUsed = kSlot + 16 + 1024;  // and alignment
     static constexpr int kBytes = D == 128 ? 231424 : 160 * 1024;
@@ -121,11 +123,6 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
@@ -200,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
     pdl_wait_prerequisites();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const char *const smem_base = smem_raw + (base - smem_u32(smem_raw));
 
     // this CTA's 256 rows: the blockIdx-th from the end over all sequences, pairs of tiles and heads
     const int B = p.bt.batch;
@@ -243,18 +241,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
     const uint32_t bars = base + S::kBars;
     const uint32_t k_full = bars, k_empty = k_full + 8 * kKS, v_full = k_empty + 8 * kKS, v_empty = v_full + 8 * kVS,
                    st_full = v_empty + 8 * kVS, s_full = st_full + 8 * kStepStages, p_full = s_full + 16, q_full = p_full + 16,
-                   o_full = q_full + 8, mx_full = o_full + 8;
+                   o_full = q_full + 8, at_full = o_full + 8;
     if (tid == 0) {
         auto init = [&](uint32_t bar, int n) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
         };
         for (int i = 0; i < kKS; ++i) init(k_full + 8 * i, 128), init(k_empty + 8 * i, 1);
-        for (int i = 0; i < kVS; ++i) init(v_full + 8 * i, 128), init(v_empty + 8 * i, 1);
+        for (int i = 0; i < kVS; ++i) init(v_full + 8 * i, kValueThreads), init(v_empty + 8 * i, 1);
         for (int i = 0; i < kStepStages; ++i) init(st_full + 8 * i, 128);
+        for (int i = 0; i < kPlaceStages; ++i) init(at_full + 8 * i, 128);
         for (int w = 0; w < 2; ++w) init(s_full + 8 * w, 1), init(p_full + 8 * w, 128);
         init(q_full, 256);
         init(o_full, 1);
-        init(mx_full, 128);
         fence_mbar_init();
     }
     if (warp == 12) {
@@ -341,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
         const int all_begin = p.causal ? (int)max((int64_t)0, (int64_t)pos0 + tile_last / p.group - p.window + 1) : 0;
 
         float ref = kNone;
-        f2 l2 = pair(0.0f, 0.0f);
+        f2 l2[4] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f), pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
         uint32_t vexp = 0x3f800000u;
         bool ok = true;
         for (int j = 0; j < steps; ++j) {
@@ -352,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 break;
             }
             tc_fence_after();
-            const uint32_t steps_at = base + S::kSteps + st * 1024, meta = base + S::kMeta + st * 32;
+            const uint32_t meta = base + S::kMeta + st * 32;
+            const float4 *const k4 = reinterpret_cast<const float4 *>(smem_base + S::kSteps + st * 1024), *const v4 = k4 + 32;
             float s[kPos];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
@@ -360,10 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
             const uint32_t vexp_new = lds32(meta + 16);
             tmem_wait_ld();
             f2 z[kPos / 2];
-            float top = -CUDART_INF_F;
 #pragma unroll
             for (int i = 0; i < kPos / 4; ++i) {
-                const float4 k = lds_f4(steps_at + 16 * i);
+                const float4 k = k4[i];
                 z[2 * i] = mul2(pair(s[4 * i], s[4 * i + 1]), pair(k.x, k.y));
                 z[2 * i + 1] = mul2(pair(s[4 * i + 2], s[4 * i + 3]), pair(k.z, k.w));
             }
@@ -386,36 +384,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                     }
                 }
             }
+            float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int i = 0; i < kPos / 2; ++i) {
                 float x, y;
                 split(z[i], x, y);
-                top = fmaxf(top, fmaxf(x, y));
+                tops[i & 3] = fmaxf(tops[i & 3], fmaxf(x, y));
             }
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             const bool over = fmaf(top, f, -ref) > kOff + kLag;
+            bool rescale = false;
+            float factor = 1.0f;
             if (__any_sync(0xffffffffu, over) || vexp_new != vexp) {
                 const float next = over ? fmaf(top, f, -kOff) : ref;
                 const float a = ex2(ref - next);
                 ref = next;
-                l2 = mul2(l2, pair(a, a));
-                if (j > 0) {
-                    // vexp / vexp_new, both powers of two
-                    const float scale = a * __uint_as_float(vexp) * __uint_as_float(0x7f000000u - vexp_new);
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(t_o + 32 * c, o);
-                        tmem_wait_ld();
-                        uint32_t lo16[16], hi16[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            lo16[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
-                            hi16[i] = __float_as_uint(__uint_as_float(o[16 + i]) * scale);
-                        }
-                        tmem_st_x16(t_o + 32 * c, lo16);
-                        tmem_st_x16(t_o + 32 * c + 16, hi16);
-                    }
-                }
+                for (int i = 0; i < 4; ++i) l2[i] = mul2(l2[i], pair(a, a));
+                // vexp / vexp_new, both powers of two
+                rescale = j > 0;
+                factor = a * __uint_as_float(vexp) * __uint_as_float(0x7f000000u - vexp_new);
                 vexp = vexp_new;
             }
             const f2 ff = pair(f, f), nref = pair(-ref, -ref);
@@ -424,15 +412,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 uint32_t h[16];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 v = lds_f4(steps_at + 512 + 128 * c + 16 * i);
+                    const float4 v = v4[8 * c + i];
                     float x[4];
                     split(fma2(z[16 * c + 2 * i], ff, nref), x[0], x[1]);
                     split(fma2(z[16 * c + 2 * i + 1], ff, nref), x[2], x[3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
                     f2 w0 = pair(x[0], x[1]), w1 = pair(x[2], x[3]);
-                    l2 = add2(l2, w0);
-                    l2 = add2(l2, w1);
+                    l2[2 * (i & 1)] = add2(l2[2 * (i & 1)], w0);
+                    l2[2 * (i & 1) + 1] = add2(l2[2 * (i & 1) + 1], w1);
                     w0 = mul2(w0, pair(v.x, v.y));
                     w1 = mul2(w1, pair(v.z, v.w));
                     split(w0, x[0], x[1]);
@@ -442,13 +430,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 }
                 tmem_st_x16(t_s + 16 * c, h);
             }
+            if (rescale) {
+                // O is complete up to the step before (its product precedes this S) and no later one has begun
+                uint32_t o[D];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) tmem_ld_32x32b_x32(t_o + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(o + 32 * c));
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < D; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) tmem_st_x16(t_o + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+            }
             tmem_wait_st();
             tc_fence_before();
             arrive(p_full + 8 * w);
         }
         // the outputs
         float l0, l1;
-        split(l2, l0, l1);
+        split(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), l0, l1);
         const float l = l0 + l1;
         if (steps > 0 && ok) ok = mbar_wait_warp(o_full, 0, p.status);
         tc_fence_after();
@@ -479,10 +478,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        const uint32_t magic[2] = {p.magic[0], p.magic[1]};
+        auto put_piece = [&](uint32_t tile, int i, int q, const uint4 &c) {  // 32 dimensions of position i
+            const uint32_t x[4] = {c.x, c.y, c.z, c.w};
+            const uint32_t row = tile + (q >> 1) * (kRows * 128) + i * 128;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put_codes(row + ((((4 * q + e) & 7) ^ (i & 7)) << 4), x[e], magic);
+        };
+        auto put_bos = [&](uint32_t tile, int q, const int8_t *c8) {  // 32 dimensions of position 0, kept at 8 bits
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+                const char4 a = *reinterpret_cast<const char4 *>(c8 + 32 * q + 8 * e), c = *reinterpret_cast<const char4 *>(c8 + 32 * q + 8 * e + 4);
+                sts128(tile + (q >> 1) * (kRows * 128) + (((4 * q + e) & 7) << 4), pack2(a.x, c.x), pack2(a.y, c.y), pack2(a.z, c.z),
+                       pack2(a.w, c.w));
+            }
+        };
         if (warp < 12) {
-            // ------------------------------------------------------------ codes -> fp16
+            // ------------------------------------------------------------ places, steps and keys
             const int i = tid - 256;  // position within the step
-            const uint32_t magic[2] = {p.magic[0], p.magic[1]};
             const uint32_t mask = (1u << p.c.page_log2) - 1;
             auto wanted = [&](int j) {
                 const int pos = (step0 + j) * kPos + i;
@@ -492,91 +505,114 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 const int at = ((step0 + j) * kPos + i) >> p.c.page_log2;
                 return wanted(j) && at < p.bt.max_pages ? __ldg(p.bt.table + (int64_t)b * p.bt.table_stride + at) : -1;
             };
-            auto row_of = [&](int j, int page) {
-                if (!wanted(j)) return kNowhere;
-                if ((unsigned)page >= (unsigned)p.c.pages) {
-                    record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
-                    return kNowhere;
+            // finds the place of this thread's position of step j and tells the others
+            auto publish = [&](int j, int page) {
+                uint32_t r = kNowhere;
+                if (wanted(j)) {
+                    if ((unsigned)page < (unsigned)p.c.pages)
+                        r = (((uint32_t)page * p.c.heads + kh) << p.c.page_log2) + (((step0 + j) * kPos + i) & mask);
+                    else
+                        record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
                 }
-                return (((uint32_t)page * p.c.heads + kh) << p.c.page_log2) + (((step0 + j) * kPos + i) & mask);
+                sts32(base + S::kPlaces + (j % kPlaceStages) * 512 + 4 * i, r);
+                arrive(at_full + 8 * (j % kPlaceStages));
+                return r;
             };
-            uint4 kc[D / 32], vc[D / 32];
-            float ks = 0.0f, vs = 0.0f;
-            auto load_keys = [&](uint32_t r) {
+            uint4 kc[D / 32];
+            float ks, vs[4];
+            // this position's key codes and step, and the value steps of the positions i % 32 + 32 k
+            auto load = [&](int j, uint32_t r) {
                 const uint4 *const src = reinterpret_cast<const uint4 *>(p.c.k_codes + (uint64_t)(r == kNowhere ? 0 : r) * (D / 2));
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) kc[c] = r != kNowhere ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
                 ks = r != kNowhere ? __ldg(p.c.k_step + r) : 0.0f;
-                vs = r != kNowhere ? __ldg(p.c.v_step + r) : 0.0f;
-            };
-            auto load_values = [&](uint32_t r) {
-                const uint4 *const src = reinterpret_cast<const uint4 *>(p.c.v_codes + (uint64_t)(r == kNowhere ? 0 : r) * (D / 2));
+                const bool ok = mbar_wait_warp(at_full + 8 * (j % kPlaceStages), (j / kPlaceStages) & 1, p.status);
+                const uint32_t places = base + S::kPlaces + (j % kPlaceStages) * 512 + 4 * lane;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) vc[c] = r != kNowhere ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            };
-            auto put_row = [&](uint32_t tile, const uint4 (&c)[D / 32]) {
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    const uint32_t x[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int g = 4 * q + e;  // eight dimensions
-                        put_codes(tile + (g >> 3) * (kRows * 128) + i * 128 + (((g & 7) ^ (i & 7)) << 4), x[e], magic);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t x = lds32(places + 128 * k);
+                    vs[k] = x != kNowhere ? __ldg(p.c.v_step + x) : 0.0f;
                 }
+                return ok;
             };
-            auto put_bos = [&](uint32_t tile, const int8_t *c8) {  // position 0 is kept at 8 bits
-                for (int g = 0; g < D / 8; ++g) {
-                    const char4 a = *reinterpret_cast<const char4 *>(c8 + 8 * g), c = *reinterpret_cast<const char4 *>(c8 + 8 * g + 4);
-                    sts128(tile + (g >> 3) * (kRows * 128) + i * 128 + (((g & 7) ^ (i & 7)) << 4), pack2(a.x, c.x), pack2(a.y, c.y),
-                           pack2(a.z, c.z), pack2(a.w, c.w));
-                }
-            };
-            uint32_t r = row_of(0, page_of(0));
+            uint32_t r = kNowhere, next = kNowhere;
             int page = page_of(1);
-            load_keys(r);
-            load_values(r);
+            bool ok = true;
+            if (steps > 0) {
+                r = publish(0, page_of(0));
+                next = publish(1, page);
+                page = page_of(2);
+                ok = load(0, r);
+            }
             uint32_t vexp = 0x0d000000u;  // 2^-101
-            for (int j = 0; j < steps; ++j) {
-                const uint32_t next = row_of(j + 1, page);
-                page = page_of(j + 2);
-                const bool live = r != kNowhere, bos = live && (step0 + j) * kPos + i == 0;
-                const int64_t bos_at = bos ? (int64_t)(r >> p.c.page_log2) * D : 0;
+            for (int j = 0; j < steps && ok; ++j) {
+                // Slot j + 2 held step j - 6.  This thread has seen k_empty of step j - 3, so the products have seen v_full of
+                // step j - 4, after which the value warps read the places of step j - 3 at the earliest.
+                const uint32_t after = j + 2 < steps ? publish(j + 2, page) : kNowhere;
+                page = page_of(j + 3);
+                const bool live = r != kNowhere;
                 const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
-                const uint32_t bits = __float_as_uint(vs) & 0x7f800000u;
-                if (bits == 0x7f800000u) vs = 0.0f, ks = CUDART_NAN_F;  // NaN for the rows that see it, and for no others
-                const uint32_t most = __reduce_max_sync(0xffffffffu, live && bits < 0x7f800000u ? bits : 0u);
-                const uint32_t maxes = base + S::kMax + (j & 1) * 16;
-                if (lane == 0) sts32(maxes + 4 * (warp - 8), most);
-                arrive(mx_full);
-                if (!mbar_wait_warp(mx_full, j & 1, p.status)) break;
-                const float4 m4 = lds_f4(maxes);
-                const uint32_t m01 = max(__float_as_uint(m4.x), __float_as_uint(m4.y)), m23 = max(__float_as_uint(m4.z), __float_as_uint(m4.w));
-                vexp = min(max(vexp, max(m01, m23)), 0x7e000000u);
-
-                const int st = j % kStepStages, sk = j % kKS, sv = j % kVS;
+                uint32_t most = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t bits = __float_as_uint(vs[k]) & 0x7f800000u;
+                    most = max(most, bits < 0x7f800000u ? bits : 0u);
+                }
+                vexp = min(max(vexp, __reduce_max_sync(0xffffffffu, most)), 0x7e000000u);
+                const float own = (warp & 2) ? ((warp & 1) ? vs[3] : vs[2]) : ((warp & 1) ? vs[1] : vs[0]);
+                const bool bad = !(fabsf(own) < CUDART_INF_F);  // NaN for the rows that see it, and for no others
+                const int st = j % kStepStages, sk = j % kKS;
+                const uint32_t steps_at = base + S::kSteps + st * 1024, meta = base + S::kMeta + st * 32, kt = base + S::kK + sk * S::kTile;
                 if (j >= kKS && !mbar_wait_warp(k_empty + 8 * sk, (j / kKS - 1) & 1, p.status)) break;
-                const uint32_t kt = base + S::kK + sk * S::kTile, steps_at = base + S::kSteps + st * 1024;
-                put_row(kt, kc);
-                if (bos) put_bos(kt, p.c.k_bos + bos_at);
-                sts32(steps_at + 4 * i, __float_as_uint(live ? ks : 0.0f));
-                sts32(steps_at + 512 + 4 * i, __float_as_uint(live ? vs * __uint_as_float(0x7f000000u - vexp) : 0.0f));
-                const uint32_t meta = base + S::kMeta + st * 32;
+                sts32(steps_at + 4 * i, __float_as_uint(bad ? CUDART_NAN_F : (live ? ks : 0.0f)));
+                sts32(steps_at + 512 + 4 * i, __float_as_uint(bad || !live ? 0.0f : own * __uint_as_float(0x7f000000u - vexp)));
                 if (lane == 0) sts32(meta + 4 * (warp - 8), live_bits);
                 if (i == 0) sts32(meta + 16, vexp);
+                arrive(st_full + 8 * st);
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) put_piece(kt, i, q, kc[q]);
+                if (live && (step0 + j) * kPos + i == 0)
+                    for (int q = 0; q < D / 32; ++q) put_bos(kt, q, p.c.k_bos + (int64_t)(r >> p.c.page_log2) * D);
                 fence_proxy_async_smem();
                 arrive(k_full + 8 * sk);
-                arrive(st_full + 8 * st);
-                load_keys(next);
-
-                if (j >= kVS && !mbar_wait_warp(v_empty + 8 * sv, (j / kVS - 1) & 1, p.status)) break;
+                if (j + 1 < steps) ok = load(j + 1, next);
+                r = next;
+                next = after;
+            }
+        } else if (warp > 12) {
+            // ------------------------------------------------------------ values
+            const int v = tid - 13 * 32;
+            constexpr int kPieces = kPos * D / 32, kRounds = (kPieces + kValueThreads - 1) / kValueThreads;
+            uint4 c[kRounds];
+            auto load = [&](int j) {  // piece x: 32 dimensions x % (D / 32) of position x / (D / 32)
+                if (!mbar_wait_warp(at_full + 8 * (j % kPlaceStages), (j / kPlaceStages) & 1, p.status)) return false;
+                const uint32_t places = base + S::kPlaces + (j % kPlaceStages) * 512;
+#pragma unroll
+                for (int k = 0; k < kRounds; ++k) {
+                    const int x = v + k * kValueThreads;
+                    const uint32_t r = x < kPieces ? lds32(places + 4 * (x / (D / 32))) : kNowhere;
+                    c[k] = r != kNowhere ? __ldg(reinterpret_cast<const uint4 *>(p.c.v_codes + (uint64_t)r * (D / 2)) + x % (D / 32))
+                                         : make_uint4(0, 0, 0, 0);
+                }
+                return true;
+            };
+            bool ok = steps > 0 && load(0);
+            for (int j = 0; j < steps && ok; ++j) {
+                const int sv = j % kVS;
                 const uint32_t vt = base + S::kV + sv * S::kTile;
-                put_row(vt, vc);
-                if (bos) put_bos(vt, p.c.v_bos + bos_at);
+                if (j >= kVS && !mbar_wait_warp(v_empty + 8 * sv, (j / kVS - 1) & 1, p.status)) break;
+#pragma unroll
+                for (int k = 0; k < kRounds; ++k) {
+                    const int x = v + k * kValueThreads;
+                    if (x < kPieces) put_piece(vt, x / (D / 32), x % (D / 32), c[k]);
+                }
+                if (step0 + j == 0 && v < D / 32) {
+                    const uint32_t r = lds32(base + S::kPlaces + (j % kPlaceStages) * 512);
+                    if (r != kNowhere) put_bos(vt, v, p.c.v_bos + (int64_t)(r >> p.c.page_log2) * D);
+                }
                 fence_proxy_async_smem();
                 arrive(v_full + 8 * sv);
-                load_values(next);
-                r = next;
+                if (j + 1 < steps) ok = load(j + 1);
             }
         } else if (warp == 12 && steps > 0) {
             // ------------------------------------------------------------ products
