@@ -138,7 +138,8 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
 // (kv4_prefill.cu).  window: INT32_MAX for none.
 cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts, int64_t qhs, const Kv4Cache &c,
                              const Kv4Batch &bt, float scale, bool causal, int window, int rows_min, void *out, float *lse,
-                             cudaStream_t s);
+                             void *ws, cudaStream_t s);
+size_t kv4_tiles_workspace(int64_t T, int group, int heads, int dim, int batch, int rows_min);
 
 // Argument rules shared by every forward entry point (the workspace is checked by
 // each entry point): BITNET_OK or the status the call returns.

@@ -796,14 +796,19 @@ cudaError_t launch_rows(RowsParams p, int64_t T, void *ws, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv4_attention_workspace(int64_t, int, int, int dim, int) {
+size_t kv4_attention_workspace(int64_t T, int q_heads, int heads, int dim, int batch) {
     // the largest of the kernels': a slot and two parts of 8 NT rows to a CTA
     auto need = [&](int resident, int nt) {
         return (size_t)sm_count() * resident * (sizeof(int4) + 2 * 8 * nt * (size_t)(dim + 2) * 4);
     };
     const size_t one = dim == 64 ? need(kResident<64, 1>, 1) : (dim == 128 ? need(kResident<128, 1>, 1) : need(kResident<256, 1>, 1));
     const size_t two = dim == 64 ? need(kResident<64, 2>, 2) : (dim == 128 ? need(kResident<128, 2>, 2) : 0);
-    return ((one > two ? one : two) + 255) & ~(size_t)255;
+    // the kernels run one after the other in the same memory
+    const int64_t rows = T * (q_heads / heads);
+    const size_t tiles = dim <= 128 && rows >= kTilesFrom ? kv4_tiles_workspace(T, q_heads / heads, heads, dim, batch, kTilesFrom) : 0;
+    size_t most = one > two ? one : two;
+    most = most > tiles ? most : tiles;
+    return (most + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_heads, int64_t qts, int64_t qhs,
@@ -821,7 +826,7 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
     p.out = out, p.lse = lse, p.status = device_status_ptr();
     p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
     if (tiles) {
-        const cudaError_t e = launch_kv4_tiles(q, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, s);
+        const cudaError_t e = launch_kv4_tiles(q, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, ws, s);
         if (e != cudaSuccess) return e;
     }
     const bool two = rows > 8;

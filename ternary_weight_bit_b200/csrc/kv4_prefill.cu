@@ -57,8 +57,18 @@ struct TileParams {
     uint16_t *out;
     float *lse;
     int *status;
+    int splits;     // CTAs that share an item's positions
+    float *part;    // [items][splits][D + 2][256]: outputs, reference, sum
+    int64_t *place;  // [items][256]: the rows' places in the output, -1 for none
     uint32_t magic[2];  // {0x64086408, 0x64806480}, as data: a logic instruction takes one constant
 };
+
+// Whether the two tiles take turns at the exponentials, so that one is at them while the other has its products
+// and its maxima.  At dim 64 the products are short and both tiles fall into step without it (a chunk of 1661
+// rows over 28000 positions: 591 us without turns, 522 with); at dim 128 the products keep them apart (440 and 460 us
+// for prompts of 9397 rows).
+template <int D>
+constexpr bool kTurns = D == 64;
 
 template <int D>
 struct Smem {
@@ -70,7 +80,7 @@ struct Smem {
     static constexpr int kMeta = kSteps + kStepStages * 1024;  // [kStepStages][8]: 4 words of live positions, the power of two
     static constexpr int kPlaces = kMeta + kStepStages * 32;   // [kPlaceStages][128]: the positions' rows in the cache
     static constexpr int kBars = kPlaces + kPlaceStages * 512;
-    static constexpr int kNumBars = 2 * kKS + 2 * kVS + kStepStages + kPlaceStages + 2 + 2 + 2;
+    static constexpr int kNumBars = 2 * kKS + 2 * kVS + kStepStages + kPlaceStages + 2 + 2 + 2 + 2;
     static constexpr int kSlot = kBars + 8 * kNumBars;
     static constexpr int kUsed = kSlot + 16 + 1024;  // and alignment
     static constexpr int kBytes = D == 128 ? 231424 : 160 * 1024;
@@ -225,8 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
         before += w < warp ? scan[w] : 0;
         total += scan[w];
     }
-    const int64_t index = total * p.c.heads - 1 - blockIdx.x;
-    if (index < 0) return;  // the same for the whole CTA
+    const int item = blockIdx.x / p.splits, part = blockIdx.x - item * p.splits;
+    const int64_t index = total * p.c.heads - 1 - item;
+    if (index < 0) {  // the same for the whole CTA: the grid is made for the most items that T rows can be
+        if (p.splits > 1 && part == 0 && tid < 2 * kRows) p.place[(int64_t)item * (2 * kRows) + tid] = -1;
+        return;
+    }
     {
         const int64_t at = index / p.c.heads;
         if (at >= before && at < before + mine) {
@@ -240,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
     }
     const uint32_t bars = base + S::kBars;
     const uint32_t k_full = bars, k_empty = k_full + 8 * kKS, v_full = k_empty + 8 * kKS, v_empty = v_full + 8 * kVS,
-                   st_full = v_empty + 8 * kVS, s_full = st_full + 8 * kStepStages, p_full = s_full + 16, q_full = p_full + 16,
+                   st_full = v_empty + 8 * kVS, s_full = st_full + 8 * kStepStages, p_full = s_full + 16, turn = p_full + 16, q_full = turn + 16,
                    o_full = q_full + 8, at_full = o_full + 8;
     if (tid == 0) {
         auto init = [&](uint32_t bar, int n) {
@@ -250,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
         for (int i = 0; i < kVS; ++i) init(v_full + 8 * i, kValueThreads), init(v_empty + 8 * i, 1);
         for (int i = 0; i < kStepStages; ++i) init(st_full + 8 * i, 128);
         for (int i = 0; i < kPlaceStages; ++i) init(at_full + 8 * i, 128);
-        for (int w = 0; w < 2; ++w) init(s_full + 8 * w, 1), init(p_full + 8 * w, 128);
+        for (int w = 0; w < 2; ++w) init(s_full + 8 * w, 1), init(p_full + 8 * w, 128), init(turn + 8 * w, 128);
         init(q_full, 256);
         init(o_full, 1);
         fence_mbar_init();
@@ -275,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
     const int row_last = min(row0 + 2 * kRows, rows) - 1;
     const int end = p.causal ? min(cap, pos0 + row_last / p.group + 1) : cap;
     const int begin = p.causal ? (int)max((int64_t)0, (int64_t)pos0 + row0 / p.group - p.window + 1) : 0;
-    const int step0 = begin / kPos;
-    const int steps = max(0, (end - step0 * kPos + kPos - 1) / kPos);
+    const int all_steps = max(0, (end - begin / kPos * kPos + kPos - 1) / kPos);
+    const int from = (int)((int64_t)all_steps * part / p.splits);
+    const int step0 = begin / kPos + from;
+    const int steps = (int)((int64_t)all_steps * (part + 1) / p.splits) - from;
     if (tid == 0 && cap < len) record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
 
     if (warp < 8) {
@@ -406,6 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 factor = a * __uint_as_float(vexp) * __uint_as_float(0x7f000000u - vexp_new);
                 vexp = vexp_new;
             }
+            if (kTurns<D> && (w == 1 || j > 0) && !mbar_wait_warp(turn + 8 * w, (w == 1 ? j : j - 1) & 1, p.status)) {
+                ok = false;
+                break;
+            }
             const f2 ff = pair(f, f), nref = pair(-ref, -ref);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -430,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 }
                 tmem_st_x16(t_s + 16 * c, h);
             }
+            if (kTurns<D>) arrive(turn + 8 * (w ^ 1));
             if (rescale) {
                 // O is complete up to the step before (its product precedes this S) and no later one has begun
                 uint32_t o[D];
@@ -451,7 +472,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
         const float l = l0 + l1;
         if (steps > 0 && ok) ok = mbar_wait_warp(o_full, 0, p.status);
         tc_fence_after();
-        if (ok) {
+        if (p.splits > 1) {
+            // the part of the output, by columns so that the rows of a warp lie side by side
+            float *const dst = p.part + ((int64_t)item * p.splits + part) * (D + 2) * (2 * kRows) + w * kRows + r;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (steps > 0) {
+                    tmem_ld_32x32b_x32(t_o + 32 * c, o);
+                    tmem_wait_ld();
+                }
+                constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};  // dimension of a group's column
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    dst[(32 * c + (i & ~7) + order[i & 7]) * (2 * kRows)] = steps > 0 && ok ? __uint_as_float(o[i]) * __uint_as_float(vexp) : 0.0f;
+            }
+            dst[D * (2 * kRows)] = ok ? ref : kNone;
+            dst[(D + 1) * (2 * kRows)] = ok ? l : 0.0f;
+            if (part == 0) p.place[(int64_t)item * (2 * kRows) + w * kRows + r] = on ? at : -1;
+        } else if (ok) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -667,8 +706,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
     }
 }
 
+// Joins the parts of 32 rows of an item, in the order of the positions.
 template <int D>
-cudaError_t launch_tiles(const TileParams &p, int64_t grid, cudaStream_t s) {
+__global__ void __launch_bounds__(256) kv4_tiles_join_kernel(const __grid_constant__ TileParams p) {
+    __shared__ float out[32][D + 1];
+    __shared__ float sums[32];
+    __shared__ int64_t places[32];
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int item = blockIdx.x >> 3, row = (blockIdx.x & 7) * 32 + lane;
+    const float *const src = p.part + (int64_t)item * p.splits * (D + 2) * (2 * kRows) + row;
+    constexpr int64_t kPart = (D + 2) * (2 * kRows);
+    const int64_t place = p.place[(int64_t)item * (2 * kRows) + row];
+    if (__syncthreads_and(place < 0)) return;  // nobody's rows, whose parts may not be written
+    float top = kNone, sum = 0.0f;
+    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, src[s * kPart + D * (2 * kRows)]);
+    for (int s = 0; s < p.splits; ++s)
+        sum = fmaf(ex2(src[s * kPart + D * (2 * kRows)] - top), src[s * kPart + (D + 1) * (2 * kRows)], sum);
+    if (warp == 0) {
+        places[lane] = place;
+        sums[lane] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (p.lse && place >= 0) p.lse[place] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+    }
+    for (int d = warp; d < D; d += 8) {
+        float y = 0.0f;
+        for (int s = 0; s < p.splits; ++s)
+            y = fmaf(ex2(src[s * kPart + D * (2 * kRows)] - top), src[s * kPart + d * (2 * kRows)], y);
+        out[lane][d] = y;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * (D / 2); i += 256) {
+        const int r = i / (D / 2), d = 2 * (i % (D / 2));
+        if (places[r] >= 0)
+            *reinterpret_cast<uint32_t *>(p.out + places[r] * D + d) = bf2(out[r][d] * sums[r], out[r][d + 1] * sums[r]);
+    }
+}
+
+template <int D>
+cudaError_t launch_tiles(const TileParams &p, int64_t items, cudaStream_t s) {
     static bool allowed[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -684,7 +760,7 @@ cudaError_t launch_tiles(const TileParams &p, int64_t grid, cudaStream_t s) {
         if (dev < kMaxDevices) allowed[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)(items * p.splits));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Smem<D>::kBytes;
     cfg.stream = s;
@@ -693,26 +769,59 @@ cudaError_t launch_tiles(const TileParams &p, int64_t grid, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_tiles_kernel<D>, p);
+    e = cudaLaunchKernelEx(&cfg, kv4_tiles_kernel<D>, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cfg.gridDim = dim3((unsigned)(items * 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv4_tiles_join_kernel<D>, p);
+}
+
+// The most items (pairs of tiles and key heads) that T rows can make: at most one pair of a sequence is not full.
+int64_t most_items(int64_t T, int group, int heads, int batch, int rows_min) {
+    const int64_t rows = T * group;
+    return (rows / (2 * kRows) + (rows / rows_min < batch ? rows / rows_min : (int64_t)batch)) * heads;
+}
+// Parts of split items: up to three of them to an SM.
+constexpr int kWaves = 3;
+int64_t most_splits(int64_t items) {
+    const int64_t s = items > 0 ? (int64_t)kWaves * sm_count() / items : 0;
+    return s < 1 ? 1 : (s > 8 ? 8 : s);
 }
 
 }  // namespace
 
+size_t kv4_tiles_workspace(int64_t T, int group, int heads, int dim, int batch, int rows_min) {
+    const int64_t items = most_items(T, group, heads, batch, rows_min), splits = most_splits(items);
+    if (splits == 1) return 0;
+    return (size_t)items * (2 * kRows) * (splits * (dim + 2) * sizeof(float) + sizeof(int64_t));
+}
+
 cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts, int64_t qhs, const Kv4Cache &c,
                              const Kv4Batch &bt, float scale, bool causal, int window, int rows_min, void *out, float *lse,
-                             cudaStream_t s) {
+                             void *ws, cudaStream_t s) {
     TileParams p = {};
     p.q = q, p.qts = qts, p.qhs = qhs, p.q_heads = q_heads, p.group = q_heads / c.heads, p.T = T;
     p.c = c, p.bt = bt, p.scale = scale, p.causal = causal, p.window = window, p.rows_min = rows_min;
     p.out = static_cast<uint16_t *>(out), p.lse = lse, p.status = device_status_ptr();
     p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
-    // at most one pair of tiles per sequence is not full
-    const int64_t rows = T * p.group;
-    const int64_t pairs = rows / (2 * kRows) + (rows < (int64_t)bt.batch * rows_min ? rows / rows_min : (int64_t)bt.batch);
-    const int64_t grid = pairs * c.heads;
-    if (grid == 0) return cudaSuccess;
-    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return c.dim == 64 ? launch_tiles<64>(p, grid, s) : launch_tiles<128>(p, grid, s);
+    const int64_t items = most_items(T, p.group, c.heads, bt.batch, rows_min);
+    if (items == 0) return cudaSuccess;
+    if (T * p.group > INT32_MAX - 2 * kRows || items * 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    // With few items the positions are split over several CTAs: as many as leave the SMs least idle, where an
+    // item costs as much as kCost steps to begin and to end.  (A chunk of 208 items with 130 steps each on 148 SMs: 522 us
+    // unsplit, in two turns of which the second fills two SMs in five; see the table of measurements.)
+    constexpr int kCost = 6;
+    const int64_t steps = ceil_div((int64_t)bt.max_pages << c.page_log2, kPos), sms = sm_count();
+    int64_t best = -1;
+    p.splits = 1;
+    for (int64_t n = 1; n <= most_splits(items) && (n == 1 || steps >= 8 * n); ++n) {
+        const int64_t cost = ceil_div(items * n, sms) * (kCost + ceil_div(steps, n) + (n > 1 ? 1 : 0));
+        if (best < 0 || cost < best) best = cost, p.splits = (int)n;
+    }
+    p.place = static_cast<int64_t *>(ws);
+    p.part = reinterpret_cast<float *>(p.place + items * (2 * kRows));
+    return c.dim == 64 ? launch_tiles<64>(p, items, s) : launch_tiles<128>(p, items, s);
 }
 
 }  // namespace bitnet
