@@ -39,10 +39,27 @@ constexpr int kPos = 128;    // positions of a step
 constexpr int kThreads = 512;
 constexpr int kValueThreads = 96;
 constexpr int kKS = 2, kVS = 2, kStepStages = 4, kPlaceStages = 8;
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;  // registers of a thread; 256 threads each
+// Registers of a thread of the two halves of the block, 256 threads each; what either lacks is spilled to an L1 that
+// shared memory leaves little of (prompts at dim 128: 472 us with 192 and 64, 420 with 184 and 72, 453 with 176 and
+// 80; a chunk at dim 64: 454, 518, 531).
+template <int D>
+constexpr int kSoftmaxRegs = D == 128 ? 184 : 192;
+template <int D>
+constexpr int kOtherRegs = 256 - kSoftmaxRegs<D>;
 constexpr uint32_t kNowhere = 0xffffffffu;
 constexpr float kOff = 3.0f, kLag = 11.0f, kNone = -3.0e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^l >= d, m = floor(2^32 (2^l - d) / d) + 1.
+struct Divide {
+    uint32_t mul, shift;
+    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift); }
+};
+Divide divide_by(uint32_t d) {
+    uint32_t l = 0;
+    while ((1u << l) < d) ++l;
+    return Divide{(uint32_t)((((uint64_t)1 << 32) * ((1ull << l) - d)) / d + 1), l};
+}
 
 struct TileParams {
     const void *q;
@@ -60,6 +77,7 @@ struct TileParams {
     int splits;     // CTAs that share an item's positions
     float *part;    // [items][splits][D + 2][256]: outputs, reference, sum
     int64_t *place;  // [items][256]: the rows' places in the output, -1 for none
+    Divide by_group;
     uint32_t magic[2];  // {0x64086408, 0x64806480}, as data: a logic instruction takes one constant
 };
 
@@ -79,7 +97,9 @@ struct Smem {
     static constexpr int kSteps = kV + kVS * kTile;            // [kStepStages][2][128] floats: key steps, value ratios
     static constexpr int kMeta = kSteps + kStepStages * 1024;  // [kStepStages][8]: 4 words of live positions, the power of two
     static constexpr int kPlaces = kMeta + kStepStages * 32;   // [kPlaceStages][128]: the positions' rows in the cache
-    static constexpr int kBars = kPlaces + kPlaceStages * 512;
+    static constexpr int kFactors = kPlaces + kPlaceStages * 512;  // [256]: the rows' factors of their scores
+    static constexpr int kOuts = kFactors + 2 * kRows * 4;         // [256] int64: the rows' places in the output, -1 for none
+    static constexpr int kBars = kOuts + 2 * kRows * 8;
     static constexpr int kNumBars = 2 * kKS + 2 * kVS + kStepStages + kPlaceStages + 2 + 2 + 2 + 2;
     static constexpr int kSlot = kBars + 8 * kNumBars;
     static constexpr int kUsed = kSlot + 16 + 1024;  // and alignment
@@ -207,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
     pdl_wait_prerequisites();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const char *const smem_base = smem_raw + (base - smem_u32(smem_raw));
+    char *const smem_base = smem_raw + (base - smem_u32(smem_raw));
 
     // this CTA's 256 rows: the blockIdx-th from the end over all sequences, pairs of tiles and heads
     const int B = p.bt.batch;
@@ -297,58 +317,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<D>));
         const int w = warp >> 2;
         const int r = tid & 127;                     // row of the tile, and lane of TMEM
         const int row = row0 + w * kRows + r;        // row of the sequence
         const bool on = row < rows;
-        const int tok = row / p.group;
-        const int64_t at = on ? (int64_t)(first + tok) * p.q_heads + kh * p.group + (row - tok * p.group) : 0;
+        const int tok = p.by_group(row);
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lane_off + w * kPos, t_o = tmem + lane_off + 2 * kPos + w * D;
 
-        // the query: scaled by a power of two into [2^14, 2^15), fp16, and the sign of the scale with it
-        float f;
+        // The tile's queries: scaled by a power of two into [2^14, 2^15), with the sign of the scale, in fp16.  D / 8 lanes
+        // share a row.
         {
-            const int64_t src = on ? (int64_t)(first + tok) * p.qts + (int64_t)(kh * p.group + (row - tok * p.group)) * p.qhs : 0;
-            const uint4 *const q = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + src);
-            uint4 raw[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) raw[i] = on ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-            uint32_t top = 0;
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    top = max(top, max((x[j] << 16) & 0x7fffffffu, x[j] & 0x7fff0000u));
-                }
+            constexpr int L = D / 8, kSets = kRows * L / 128;
+            const int piece = lane % L;
+            const uint32_t mine = base + S::kQ + w * S::kTile + (piece >> 3) * (kRows * 128);
+            auto row_at = [&](int i) { return (i * 4 + (warp & 3)) * (32 / L) + lane / L; };
+            auto at = [&](int rr) { return mine + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4); };
+            // each lane brings its 8 values to where their fp16 belongs, ...
+#pragma unroll 4
+            for (int i = 0; i < kSets; ++i) {
+                const int rr = row_at(i), rw = row0 + w * kRows + rr;
+                const int tk = p.by_group(rw), head = kh * p.group + (rw - tk * p.group);
+                const uint16_t *const src = reinterpret_cast<const uint16_t *>(p.q) +
+                                            (rw < rows ? (int64_t)(first + tk) * p.qts + (int64_t)head * p.qhs + 8 * piece : 0);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(rr)), "l"(src), "r"(rw < rows ? 16 : 0) : "memory");
+                if (piece == 0)
+                    *reinterpret_cast<int64_t *>(smem_base + S::kOuts + 8 * (w * kRows + rr)) =
+                        rw < rows ? (int64_t)(first + tk) * p.q_heads + head : -1;
             }
-            bad = top > 0x7f800000u;  // a NaN: the row's other values do not matter
-            const uint32_t up_bits = min(max(0x86000000u - (top & 0x7f800000u), 0x07800000u), 0x7e800000u);
-            const float up = top > 0 && !bad ? __uint_as_float(up_bits) : 1.0f;
-            const float sup = p.scale < 0.0f ? -up : up;
-            f = fmaxf(fabsf(p.scale) * kLog2e * (1.0f / up), 1.0e-37f);
-            const uint32_t dst = base + S::kQ + w * S::kTile + r * 128;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            // ... and turns them into it there
+#pragma unroll 4
+            for (int i = 0; i < kSets; ++i) {
+                const int rr = row_at(i);
+                uint32_t x[4], top = 0;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at(rr)) : "memory");
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                for (int j = 0; j < 4; ++j) top = max(top, max((x[j] << 16) & 0x7fffffffu, x[j] & 0x7fff0000u));
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const uint32_t up_bits = min(max(0x86000000u - (top & 0x7f800000u), 0x07800000u), 0x7e800000u);
+                // a NaN: the row's other values do not matter
+                const float up = top > 0 && top <= 0x7f800000u ? __uint_as_float(up_bits) : 1.0f;
+                const float sup = p.scale < 0.0f ? -up : up;
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     y[2 * j] = __uint_as_float(x[j] << 16) * sup;
                     y[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u) * sup;
                 }
-                sts128(dst + (i >> 3) * (kRows * 128) + (((i & 7) ^ (r & 7)) << 4), pack2(y[0], y[4]), pack2(y[1], y[5]),
-                       pack2(y[2], y[6]), pack2(y[3], y[7]));
+                sts128(at(rr), pack2(y[0], y[4]), pack2(y[1], y[5]), pack2(y[2], y[6]), pack2(y[3], y[7]));
+                if (piece == 0)  // 1 / up, a power of two
+                    sts32(base + S::kFactors + 4 * (w * kRows + rr),
+                          __float_as_uint(fmaxf(fabsf(p.scale) * kLog2e * __uint_as_float(0x7f000000u - __float_as_uint(up)), 1.0e-37f)));
             }
             fence_proxy_async_smem();
             arrive(q_full);
         }
+        bool ok = mbar_wait_warp(q_full, 0, p.status);
+        const float f = __uint_as_float(lds32(base + S::kFactors + 4 * (w * kRows + r)));  // of this row's scores, with log2 e
 
         // positions that this row sees, and those that all rows of the tile see
-        const int tile_first = (row0 + w * kRows) / p.group, tile_last = min(row0 + (w + 1) * kRows, rows) - 1;
+        const int tile_first = p.by_group(row0 + w * kRows), tile_last = min(row0 + (w + 1) * kRows, rows) - 1;
         const int my_end = p.causal && on ? pos0 + tok + 1 : INT32_MAX;
         const int my_begin = p.causal && on ? (int)max((int64_t)0, (int64_t)pos0 + tok - p.window + 1) : 0;
         const int all_end = p.causal ? min(cap, pos0 + tile_first + 1) : cap;
@@ -357,8 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
         float ref = kNone;
         f2 l2[4] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f), pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
         uint32_t vexp = 0x3f800000u;
-        bool ok = true;
-        for (int j = 0; j < steps; ++j) {
+        for (int j = 0; j < steps && ok; ++j) {
             const int at0 = (step0 + j) * kPos;
             const int st = j % kStepStages;
             if (!mbar_wait_warp(s_full + 8 * w, j & 1, p.status) || !mbar_wait_warp(st_full + 8 * st, (j / kStepStages) & 1, p.status)) {
@@ -472,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
         const float l = l0 + l1;
         if (steps > 0 && ok) ok = mbar_wait_warp(o_full, 0, p.status);
         tc_fence_after();
+        const int64_t *const place = reinterpret_cast<const int64_t *>(smem_base + S::kOuts) + w * kRows;
         if (p.splits > 1) {
             // the part of the output, by columns so that the rows of a warp lie side by side
             float *const dst = p.part + ((int64_t)item * p.splits + part) * (D + 2) * (2 * kRows) + w * kRows + r;
@@ -489,10 +520,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
             }
             dst[D * (2 * kRows)] = ok ? ref : kNone;
             dst[(D + 1) * (2 * kRows)] = ok ? l : 0.0f;
-            if (part == 0) p.place[(int64_t)item * (2 * kRows) + w * kRows + r] = on ? at : -1;
+            if (part == 0) p.place[(int64_t)item * (2 * kRows) + w * kRows + r] = place[r];
         } else if (ok) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
+            // rows of bf16 over the tile of Q, which no product reads any more; 16-byte pieces swizzled by row
+            const float inv = l == 0.0f ? 0.0f : __uint_as_float(vexp) / l;
+            constexpr int P = D / 8;  // pieces of a row
+            const uint32_t rows_at = base + S::kQ + w * S::kTile + (r & ~31) * P * 16;  // the warp's 32 rows
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 if (steps > 0) {
@@ -502,21 +536,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0;
                 }
-                if (on) {
-                    uint4 *const dst = reinterpret_cast<uint4 *>(p.out + at * D + 32 * c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float y[8];
+                for (int i = 0; i < 4; ++i) {
+                    float y[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * i + e]) * __uint_as_float(vexp) * inv;
-                        dst[i] = make_uint4(bf2(y[0], y[2]), bf2(y[4], y[6]), bf2(y[1], y[3]), bf2(y[5], y[7]));
-                    }
+                    for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * i + e]) * inv;
+                    sts128(rows_at + (lane * P + ((4 * c + i) ^ (lane & 7))) * 16, bf2(y[0], y[2]), bf2(y[4], y[6]), bf2(y[1], y[3]), bf2(y[5], y[7]));
                 }
             }
-            if (on && p.lse) p.lse[at] = l == 0.0f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+            if (p.lse && on) p.lse[place[r]] = l == 0.0f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+            __syncwarp();
+#pragma unroll 2
+            for (int i = 0; i < P; ++i) {
+                const int rr = (i * 32 + lane) / P, piece = lane % P;
+                uint32_t y[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(rows_at + (rr * P + (piece ^ (rr & 7))) * 16)
+                             : "memory");
+                const int64_t to = place[(r & ~31) + rr];
+                if (to >= 0) *reinterpret_cast<uint4 *>(p.out + to * D + 8 * piece) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
         const uint32_t magic[2] = {p.magic[0], p.magic[1]};
         auto put_piece = [&](uint32_t tile, int i, int q, const uint4 &c) {  // 32 dimensions of position i
             const uint32_t x[4] = {c.x, c.y, c.z, c.w};
@@ -756,7 +799,7 @@ cudaError_t launch_tiles(const TileParams &p, int64_t items, cudaStream_t s) {
         cudaFuncAttributes at;
         e = cudaFuncGetAttributes(&at, (const void *)kv4_tiles_kernel<D>);
         if (e != cudaSuccess) return e;
-        if (at.numRegs * kThreads < 256 * (kSoftmaxRegs + kOtherRegs)) return cudaErrorInvalidConfiguration;
+        if (at.numRegs * kThreads < 256 * (kSoftmaxRegs<D> + kOtherRegs<D>)) return cudaErrorInvalidConfiguration;
         if (dev < kMaxDevices) allowed[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
@@ -805,6 +848,7 @@ cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts,
     p.c = c, p.bt = bt, p.scale = scale, p.causal = causal, p.window = window, p.rows_min = rows_min;
     p.out = static_cast<uint16_t *>(out), p.lse = lse, p.status = device_status_ptr();
     p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
+    p.by_group = divide_by((uint32_t)p.group);
     const int64_t items = most_items(T, p.group, c.heads, bt.batch, rows_min);
     if (items == 0) return cudaSuccess;
     if (T * p.group > INT32_MAX - 2 * kRows || items * 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
