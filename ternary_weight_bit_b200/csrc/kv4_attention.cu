@@ -58,9 +58,9 @@ struct Ring {
 };
 // Tiles of a warp under way at a time: what fits the shared memory of an SM with kResident CTAs.
 template <int D, int NT>
-constexpr int kResident = D * NT == 64 || (D == 128 && NT == 1) ? 4 : (D == 64 ? 3 : 2);
+constexpr int kResident = D == 64 && NT == 1 ? 3 : 2;
 template <int D, int NT>
-constexpr int kStages = D == 128 && NT == 2 ? 5 : (D == 64 ? 5 : 3);
+constexpr int kStages = D == 256 ? 3 : 5;
 template <int D, int NT>
 constexpr int kRowsSmem = (int)(kStages<D, NT> * Ring<D>::kStage) > 8 * NT * (D + 4) * 4 ? kWarps * (int)(kStages<D, NT> * Ring<D>::kStage)
                                                                                       : kWarps * 8 * NT * (D + 4) * 4;
