@@ -12,6 +12,8 @@
 // warp takes 256 / D rows at a time; kIter such sets are loaded before the first is used.
 // A CTA takes a few tokens and a part of their 2 * heads rows; it looks its tokens' places up
 // once, into shared memory, while its first rows are on their way.
+#include <type_traits>
+
 #include "kv4.cuh"
 
 namespace bitnet {
@@ -24,23 +26,22 @@ constexpr int kMaxTokens = 4;  // tokens of a CTA
 template <int D>
 constexpr int kPerCta = kWarps * (256 / D) * kIter;  // rows of a CTA
 
+// A lane's 8 values of a row, as they lie in memory.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *x, int64_t i, float *v) {
-    if constexpr (BF16) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(x) + i));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw {
+    uint4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *x, int64_t i, bool on) {
+        const uint4 *const p = reinterpret_cast<const uint4 *>(static_cast<const char *>(x) + i * (BF16 ? 2 : 4));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-    } else {
-        const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x) + i);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        for (int j = 0; j < (BF16 ? 1 : 2); ++j) w[j] = on ? __ldg(p + j) : make_uint4(0, 0, 0, 0);
     }
-}
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[BF16 ? 0 : 1].x, w[BF16 ? 0 : 1].y, w[BF16 ? 0 : 1].z, w[BF16 ? 0 : 1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = __uint_as_float(!BF16 ? u[j] : (j % 2 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16));
+    }
+};
 
 // Where a token stands.
 struct Place {
@@ -69,21 +70,20 @@ __device__ __forceinline__ void locate_tokens(const Kv4Cache &c, const Kv4Batch 
     __syncthreads();
 }
 
-// A row of a CTA: its token (fastest, so that the rows of one warp lie side by side in the
-// cache), head and side (0 keys, 1 values).
-struct RowId {
-    int tok, head, side;
-    bool live;
+// A lane's rows: one token, and of its 2 * heads rows (keys, then values) every step-th.
+template <int D>
+struct Rows {
+    static constexpr int LPR = D / 8, RP = 32 / LPR;
+    static_assert(kWarps * RP % kMaxTokens == 0, "a lane keeps its token");
+    int tok, first, step;
+    __device__ __forceinline__ Rows(int tokens_log2) {
+        const int r = blockIdx.y * kPerCta<D> + (threadIdx.x >> 5) * RP + (threadIdx.x & 31) / LPR;
+        tok = r & ((1 << tokens_log2) - 1);
+        first = r >> tokens_log2;
+        step = (kWarps * RP) >> tokens_log2;
+    }
+    __device__ __forceinline__ int row(int it) const { return first + it * step; }
 };
-__device__ __forceinline__ RowId row_id(int r, int tokens_log2, int heads, int rows) {
-    RowId id;
-    id.live = r < rows;
-    id.tok = r & ((1 << tokens_log2) - 1);
-    const int hs = r >> tokens_log2;
-    id.side = hs >= heads;
-    id.head = id.side ? hs - heads : hs;
-    return id;
-}
 
 // A NaN in a row makes its step NaN, so that it is not lost.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -91,162 +91,196 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves rne(t) in the low mantissa bits
 
-// Writing.  The code is decided in fp32 where that is safe and in fp64 otherwise: the fp32
-// product t = x * (Q / scale) is within 16 roundings (7 adds in a lane, 5 in the tree, the
-// mean's and scale's additions and divisions, the product) of the exact one, below 1e-6
-// relative, so a t further than 1.25e-6 * max|code| from a half-integer rounds as the exact
-// value does.  About 1 row in 200 of 4-bit rows has a value nearer than that, and its warp
-// forms the statistic and the products again in fp64.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(32 * kWarps)
+// Writing.  A code is decided in fp32 where that is safe and in fp64 otherwise.  In fp32 it is
+// level = rne(n * u) with u = x / scale * (Q / n) + zero / n clamped to [0, 1] by the addition
+// itself, n + 1 levels from -zero on.  u * n is off by at most 17 roundings of x Q / scale (7
+// adds in a lane, 5 in the tree, the scale's addition, the reciprocal at two, the constant and
+// its product), 17 * 2^-24 zero, and the roundings of u and zero / n, n 2^-24: together below
+// 1.15e-6 zero.  So where n u is further than 1.25e-6 zero from a half-integer, its level is the
+// exact value's.  About 1 row in 200 of 4-bit rows has a value nearer than that; its warp, and
+// that of a position 0, forms the statistic and the products again in fp64.
+template <bool BF16, int D, int BITS>
+__global__ void __launch_bounds__(32 * kWarps, BF16 ? 4 : 3)
 kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t T, int64_t kts, int64_t khs,
-                 int64_t vts, int64_t vhs, Kv4Cache c, Kv4Batch bt, int bits, float eps, int tokens_log2, int rows,
-                 int *status) {
-    constexpr int LPR = D / 8, RP = 32 / LPR;
+                 int64_t vts, int64_t vhs, Kv4Cache c, Kv4Batch bt, float eps, int tokens_log2, int *status) {
+    constexpr int LPR = D / 8;
+    static_assert(kIter <= LPR, "lane i of a row keeps the step of iteration i");
+    constexpr double kQ = BITS == 4 ? 2.6457513110645905905 : 3.0;
+    constexpr float kZero = BITS == 4 ? 8.0f : 4.0f, kLevels = 2.0f * kZero - 1.0f;
     __shared__ Place place[kMaxTokens];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const int p = lane % LPR;
     const int t0 = blockIdx.x << tokens_log2;
-    const int r0 = blockIdx.y * kPerCta<D> + warp * RP;
-    float x[kIter][8];
+    const Rows<D> id(tokens_log2);
+    const int heads = c.heads;
+    Raw<BF16> raw[kIter];
+    {
+        const bool on = t0 + id.tok < T;
+        const int64_t from_k = (t0 + id.tok) * kts + 8 * p, from_v = (t0 + id.tok) * vts + 8 * p - heads * vhs;
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-        const RowId id = row_id(r0 + it * kWarps * RP + lane / LPR, tokens_log2, c.heads, rows);
-        if (id.live && t0 + id.tok < T) {
-            load8<BF16>(id.side ? v : k, (t0 + id.tok) * (id.side ? vts : kts) + id.head * (id.side ? vhs : khs) + 8 * p,
-                        x[it]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[it][e] = 0.0f;
+        for (int it = 0; it < kIter; ++it) {
+            const int hs = id.row(it);
+            const bool side = hs >= heads;
+            raw[it].load(side ? v : k, side ? from_v + hs * vhs : from_k + hs * khs, on && hs < 2 * heads);
         }
     }
     locate_tokens(c, bt, t0, 1 << tokens_log2, T, status, place);
+    const Place at = place[id.tok];
+    const int64_t row0 = kv4_rows(c, max(at.page, 0), 0) + at.row;
+    const bool bos = at.pos == 0;
+    float own = 0.0f;  // of iteration p: the scale, or the step where fp64 gave it
+    bool is_step = false;
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-        const int r = r0 + it * kWarps * RP;
-        if (r >= rows) break;  // uniform in the warp
-        const RowId id = row_id(r + lane / LPR, tokens_log2, c.heads, rows);
-        const Place at = id.live ? place[id.tok] : Place{-1, 0, -1};
-        // the rows of a warp may differ in kind; every lane takes the same shuffles
-        const bool bos = at.pos == 0;
-        const bool mean = !bos && bits == 4;
-        float a = 0.0f;
+        const int hs = id.row(it);
+        if (__all_sync(0xffffffffu, hs >= 2 * heads)) break;
+        float x[8], a = 0.0f;
+        raw[it].values(x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a = mean ? a + fabsf(x[it][e]) : max_nan(a, fabsf(x[it][e]));
+        for (int e = 0; e < 8; ++e) a = BITS == 4 ? a + fabsf(x[e]) : max_nan(a, fabsf(x[e]));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) {
             const float b = __shfl_xor_sync(0xffffffffu, a, o);
-            a = mean ? a + b : max_nan(a, b);
+            a = BITS == 4 ? a + b : max_nan(a, b);
         }
-        const float q = bos ? 127.0f : (bits == 4 ? 2.64575131106459059f : 3.0f);
-        const float lo = bos ? -128.0f : (bits == 4 ? -8.0f : -4.0f);
-        const float scale = __fadd_rn(mean ? a * (1.0f / D) : a, eps);
-        const float s = __fdiv_rn(q, scale);
-        float step = __fdiv_rn(scale, q);
-        float t[8];
-        bool near = !(scale <= 3.0e38f && s <= 3.0e38f);  // beyond fp32
+        const float scale = __fadd_rn(BITS == 4 ? a * (1.0f / D) : a, eps);
+        const float s = (float)(kQ / kLevels) * rcp(scale);
+        float f[8], most = 0.0f;  // levels, and how far the farthest value is from its own
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float y = s * x[it][e];
-            const float z = fminf(fmaxf(y, lo), -1.0f - lo);
-            t[e] = __fadd_rn(z, kMagic);
-            near |= fabsf(fabsf(z - __fsub_rn(t[e], kMagic)) - 0.5f) < -1.25e-6f * lo;
+            const float u = __saturatef(fmaf(x[e], s, kZero / kLevels));
+            f[e] = __fsub_rn(fmaf(u, kLevels, kMagic), kMagic);
+            most = fmaxf(most, fabsf(fmaf(u, kLevels, -f[e])));
         }
-        const uint32_t nears = __ballot_sync(0xffffffffu, near);
-        if (nears) {
-            // only the rows that ask for it change, so that a row's step does not depend on its neighbours
-            const bool mine = (nears >> (lane & ~(LPR - 1)) & (0xffffffffu >> (32 - LPR))) != 0;
-            double w = 0.0;
+        // four levels to the low 16 bits of a float; level - zero in two's complement is (level + 8 - zero) ^ 8
+        const float lo = fmaf(fmaf(fmaf(f[3] + 2048.0f, 16.0f, f[2]), 16.0f, f[1]), 16.0f, f[0]);
+        const float hi = fmaf(fmaf(fmaf(f[7] + 2048.0f, 16.0f, f[6]), 16.0f, f[5]), 16.0f, f[4]);
+        uint32_t w = (__byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410) + (BITS == 4 ? 0u : 0x44444444u)) ^ 0x88888888u;
+        if (p == it) own = scale;
+        const bool live = at.page >= 0 && hs < 2 * heads, side = hs >= heads;
+        const int head = side ? hs - heads : hs;
+        const uint32_t asks = __ballot_sync(0xffffffffu, bos || !(scale >= 1e-36f && scale <= 1e36f && most < 0.5f - 1.25e-6f * kZero));
+        if (asks) {
+            // the rows of a warp may differ in kind; every lane takes the same shuffles, and only
+            // the rows that ask for it change, so that a row's step does not depend on its neighbours
+            const bool mean = BITS == 4 && !bos;
+            double sum = 0.0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const double m = fabs((double)x[it][e]);
-                w = mean ? w + m : fmax(w, m);
+                const double m = fabs((double)x[e]);
+                sum = mean ? sum + m : fmax(sum, m);
             }
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) {
-                const double b = __shfl_xor_sync(0xffffffffu, w, o);
-                w = mean ? w + b : fmax(w, b);
+                const double b = __shfl_xor_sync(0xffffffffu, sum, o);
+                sum = mean ? sum + b : fmax(sum, b);
             }
-            const double qd = bos ? 127.0 : (bits == 4 ? 2.6457513110645905905 : 3.0);
-            const double sd = (mean ? w / D : w) + (double)eps;
-            if (mine) step = scale != scale ? scale : (float)(sd / qd);
+            float nan = fabsf(x[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double y = fmin(fmax((double)x[it][e] * (qd / sd), (double)lo), -1.0 - (double)lo);
-                if (mine) t[e] = __fadd_rn((float)rint(y), kMagic);
+            for (int e = 1; e < 8; ++e) nan = max_nan(nan, fabsf(x[e]));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) nan = max_nan(nan, __shfl_xor_sync(0xffffffffu, nan, o));
+            if (asks >> (lane & ~(LPR - 1)) & (0xffffffffu >> (32 - LPR))) {
+                const double q = bos ? 127.0 : kQ, zero = bos ? 128.0 : (double)kZero;
+                const double sd = (mean ? sum / D : sum) + (double)eps;
+                if (p == it) own = nan != nan ? nan : (float)(sd / q), is_step = true;
+                const double qs = q / sd;
+                uint32_t w8[2] = {};
+                w = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t code = (uint32_t)(int)rint(fmin(fmax((double)x[e] * qs, -zero), zero - 1.0));
+                    w |= (code & 15u) << (4 * e);
+                    w8[e >> 2] |= (code & 255u) << (8 * (e & 3));
+                }
+                if (bos && live)
+                    *reinterpret_cast<uint2 *>((side ? c.v_bos : c.k_bos) + ((int64_t)at.page * heads + head) * D + 8 * p) =
+                        make_uint2(w8[0], w8[1]);
             }
         }
-        if (at.page < 0) continue;
-        const int64_t row = kv4_rows(c, at.page, id.head) + at.row;
-        uint32_t w = 0, w0 = 0, w1 = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w |= (__float_as_uint(t[e]) & 15u) << (4 * e);
-        *reinterpret_cast<uint32_t *>((id.side ? c.v_codes : c.k_codes) + row * (D / 2) + 4 * p) = w;
-        if (p == 0) (id.side ? c.v_step : c.k_step)[row] = step;
-        if (bos) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w0 |= (__float_as_uint(t[e]) & 255u) << (8 * e);
-                w1 |= (__float_as_uint(t[e + 4]) & 255u) << (8 * e);
-            }
-            *reinterpret_cast<uint2 *>((id.side ? c.v_bos : c.k_bos) + ((int64_t)at.page * c.heads + id.head) * D + 8 * p) =
-                make_uint2(w0, w1);
-        }
+        if (live)
+            *reinterpret_cast<uint32_t *>((side ? c.v_codes : c.k_codes) + (row0 + ((int64_t)head << c.page_log2)) * (D / 2) + 4 * p) = w;
+    }
+    const int hs = id.row(p);
+    if (p < kIter && hs < 2 * heads && at.page >= 0) {
+        const bool side = hs >= heads;
+        (side ? c.v_step : c.k_step)[row0 + ((int64_t)(side ? hs - heads : hs) << c.page_log2)] =
+            is_step ? own : __fdiv_rn(own, (float)kQ);
     }
 }
 
-// Reading back: value = step * code.
+// Reading back: value = step * code.  Nibble e of a word plus 8, put into the mantissa of
+// 2^(23 - 4 e), is that plus the nibble exactly; less 2^(23 - 4 e) + 8 it is the code.
+// Lane p of a row writes values 8 p .. 8 p + 7 of it (bf16), or 4 p .. and 4 (p + D / 8) .. (fp32),
+// so that a store's lanes lie side by side.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(32 * kWarps)
 kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, void *__restrict__ v_out,
-                int tokens_log2, int rows, int *status) {
-    constexpr int LPR = D / 8, RP = 32 / LPR;
+                int tokens_log2, int *status) {
+    constexpr int LPR = D / 8;
     __shared__ Place place[kMaxTokens];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int p = lane % LPR;
+    const int p = (threadIdx.x & 31) % LPR;
     const int t0 = blockIdx.x << tokens_log2;
+    const Rows<D> id(tokens_log2);
+    const int heads = c.heads;
     locate_tokens(c, bt, t0, 1 << tokens_log2, T, status, place);
-    const int r0 = blockIdx.y * kPerCta<D> + warp * RP;
+    const Place at = place[id.tok];
+    if (at.pos == INT32_MIN) return;
+    const bool on = at.page >= 0, bos = at.pos == 0;
+    const int64_t row0 = kv4_rows(c, max(at.page, 0), 0) + at.row;
     uint32_t w[kIter];
-    uint2 w8[kIter];
     float step[kIter];
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-        const RowId id = row_id(r0 + it * kWarps * RP + lane / LPR, tokens_log2, c.heads, rows);
-        const Place at = id.live ? place[id.tok] : Place{-1, 0, -1};
-        w[it] = 0, step[it] = 0.0f, w8[it] = make_uint2(0, 0);
-        if (at.page >= 0) {
-            const int64_t row = kv4_rows(c, at.page, id.head) + at.row;
-            step[it] = (id.side ? c.v_step : c.k_step)[row];
-            if (at.pos == 0)
-                w8[it] = *reinterpret_cast<const uint2 *>((id.side ? c.v_bos : c.k_bos) +
-                                                          ((int64_t)at.page * c.heads + id.head) * D + 8 * p);
-            else
-                w[it] = *reinterpret_cast<const uint32_t *>((id.side ? c.v_codes : c.k_codes) + row * (D / 2) + 4 * p);
+        const int hs = id.row(it);
+        const bool side = hs >= heads;
+        w[it] = 0x88888888u, step[it] = 0.0f;
+        if (on && hs < 2 * heads) {
+            const int64_t row = row0 + ((int64_t)(side ? hs - heads : hs) << c.page_log2);
+            const uint8_t *const codes = (side ? c.v_codes : c.k_codes) + row * (D / 2);
+            step[it] = (side ? c.v_step : c.k_step)[row];
+            if constexpr (BF16) {
+                w[it] = *reinterpret_cast<const uint32_t *>(codes + 4 * p);
+            } else {
+                const uint16_t *const c16 = reinterpret_cast<const uint16_t *>(codes) + p;
+                w[it] = c16[0] | (uint32_t)c16[LPR] << 16;
+            }
         }
     }
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-        const RowId id = row_id(r0 + it * kWarps * RP + lane / LPR, tokens_log2, c.heads, rows);
-        if (!id.live) continue;
-        const Place at = place[id.tok];
-        void *out = id.side ? v_out : k_out;
-        if (at.pos == INT32_MIN || !out) continue;
+        const int hs = id.row(it);
+        const bool side = hs >= heads;
+        void *const out = side ? v_out : k_out;
+        if (hs >= 2 * heads || !out) continue;
+        const int head = side ? hs - heads : hs;
         float y[8];
+        if (bos) {
+            const int8_t *const c8 = (side ? c.v_bos : c.k_bos) + ((int64_t)max(at.page, 0) * heads + head) * D;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int code = at.pos == 0 ? (int)(int8_t)((e < 4 ? w8[it].x : w8[it].y) >> (8 * (e & 3)))
-                                         : (int)(w[it] << (28 - 4 * e)) >> 28;
-            y[e] = step[it] * (float)code;
+            for (int e = 0; e < 8; ++e) y[e] = on ? step[it] * (float)c8[BF16 ? 8 * p + e : 4 * p + (e & 3) + (e >> 2) * (D / 2)] : 0.0f;
+        } else {
+            const uint32_t u[2] = {w[it] ^ 0x88888888u, (w[it] ^ 0x88888888u) >> 16};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t one = (uint32_t)(127 + 23 - 4 * (e & 3)) << 23;  // 2^(23 - 4 (e % 4)): its bit 4 (e % 4) counts 1
+                const float base = __uint_as_float(one | 8u << (4 * (e & 3)));
+                y[e] = step[it] * __fsub_rn(__uint_as_float((u[e >> 2] & (15u << (4 * (e & 3)))) | one), base);
+            }
         }
-        const int64_t o = ((int64_t)(t0 + id.tok) * c.heads + id.head) * D + 8 * p;
+        const int64_t o = ((int64_t)(t0 + id.tok) * heads + head) * D;
         if constexpr (BF16) {
             uint32_t h[4];
 #pragma unroll
@@ -254,18 +288,18 @@ kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, vo
                 const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
                 h[e] = *reinterpret_cast<const uint32_t *>(&b);
             }
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + o) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + o + 8 * p) = make_uint4(h[0], h[1], h[2], h[3]);
         } else {
-            float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + o);
-            d[0] = make_float4(y[0], y[1], y[2], y[3]);
-            d[1] = make_float4(y[4], y[5], y[6], y[7]);
+            float *const d = reinterpret_cast<float *>(out) + o + 4 * p;
+            *reinterpret_cast<float4 *>(d) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4 *>(d + D / 2) = make_float4(y[4], y[5], y[6], y[7]);
         }
     }
 }
 
 struct RowGrid {
     dim3 grid;
-    int tokens_log2, rows;
+    int tokens_log2;
 };
 // Tokens of a CTA: four where that leaves at least eight CTAs to an SM (neighbouring rows
 // of the cache are then moved together), one otherwise.
@@ -276,8 +310,7 @@ RowGrid row_grid(int64_t T, int heads, int D) {
     while (g.tokens_log2 < 2 && ceil_div(T, 2 << g.tokens_log2) * ceil_div((int64_t)2 * heads << (g.tokens_log2 + 1), per_round) >=
                                     8 * (int64_t)sm_count())
         ++g.tokens_log2;
-    g.rows = (2 * heads) << g.tokens_log2;
-    g.grid = dim3((unsigned)ceil_div(T, 1 << g.tokens_log2), (unsigned)ceil_div(g.rows, per_round));
+    g.grid = dim3((unsigned)ceil_div(T, 1 << g.tokens_log2), (unsigned)ceil_div((int64_t)2 * heads << g.tokens_log2, per_round));
     return g;
 }
 
@@ -301,13 +334,17 @@ cudaError_t launch_kv4_write(const void *k, const void *v, bool bf16, int64_t T,
                              int64_t vhs, const Kv4Cache &c, const Kv4Batch &bt, int bits, float eps, cudaStream_t s) {
     const RowGrid g = row_grid(T, c.heads, c.dim);
     int *status = device_status_ptr();
-    auto go = [&](auto kernel) {
-        return launch_rows(kernel, g.grid, s, k, v, T, kts, khs, vts, vhs, c, bt, bits, eps, g.tokens_log2, g.rows,
-                           status);
+    auto go = [&](auto kernel) { return launch_rows(kernel, g.grid, s, k, v, T, kts, khs, vts, vhs, c, bt, eps, g.tokens_log2, status); };
+    auto of = [&](auto type, auto n) {
+        constexpr bool kBf16 = decltype(type)::value;
+        constexpr int kBits = decltype(n)::value;
+        if (c.dim == 64) return go(kv4_write_kernel<kBf16, 64, kBits>);
+        if (c.dim == 128) return go(kv4_write_kernel<kBf16, 128, kBits>);
+        return go(kv4_write_kernel<kBf16, 256, kBits>);
     };
-    if (c.dim == 64) return bf16 ? go(kv4_write_kernel<true, 64>) : go(kv4_write_kernel<false, 64>);
-    if (c.dim == 128) return bf16 ? go(kv4_write_kernel<true, 128>) : go(kv4_write_kernel<false, 128>);
-    return bf16 ? go(kv4_write_kernel<true, 256>) : go(kv4_write_kernel<false, 256>);
+    using std::integral_constant;
+    if (bits == 4) return bf16 ? of(std::true_type(), integral_constant<int, 4>()) : of(std::false_type(), integral_constant<int, 4>());
+    return bf16 ? of(std::true_type(), integral_constant<int, 3>()) : of(std::false_type(), integral_constant<int, 3>());
 }
 
 cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &bt, int64_t T, void *k_out, void *v_out, bool bf16,
@@ -315,7 +352,7 @@ cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &bt, int64_t T, vo
     const RowGrid g = row_grid(T, c.heads, c.dim);
     int *status = device_status_ptr();
     auto go = [&](auto kernel) {
-        return launch_rows(kernel, g.grid, s, c, bt, T, k_out, v_out, g.tokens_log2, g.rows, status);
+        return launch_rows(kernel, g.grid, s, c, bt, T, k_out, v_out, g.tokens_log2, status);
     };
     if (c.dim == 64) return bf16 ? go(kv4_read_kernel<true, 64>) : go(kv4_read_kernel<false, 64>);
     if (c.dim == 128) return bf16 ? go(kv4_read_kernel<true, 128>) : go(kv4_read_kernel<false, 128>);
