@@ -9,9 +9,10 @@
 //
 // Both kernels are HBM-bound: a row is read once and written once.  A lane owns 8
 // neighbouring values (one 32-bit word of codes), so LPR = D / 8 lanes share a row and a
-// warp takes 256 / D rows at a time; kIter such sets are loaded before the first is used.
-// A CTA takes a few tokens and a part of their 2 * heads rows; it looks its tokens' places up
-// once, into shared memory, while its first rows are on their way.
+// warp takes 256 / D rows at a time; four such sets (reading: eight) are loaded before the first is used.
+// A CTA takes a few tokens and a part of their heads, half of its warps the keys and half the
+// values; it looks its tokens' places up once, into shared memory (a write's first rows are on
+// their way meanwhile).
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -21,17 +22,18 @@ namespace bitnet {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kIter = 4;       // row sets in flight per warp
-constexpr int kMaxTokens = 4;  // tokens of a CTA
+constexpr int kWriteIter = 4, kReadIter = 8;  // row sets in flight per warp
 template <int D>
-constexpr int kPerCta = kWarps * (256 / D) * kIter;  // rows of a CTA
+constexpr int kSet = kWarps / 2 * (256 / D);  // rows that a side's warps take at a time
+template <int D>
+constexpr int kMaxTokens = kSet<D> < 16 ? kSet<D> : 16;  // tokens of a CTA
 
 // A lane's 8 values of a row, as they lie in memory.
 template <bool BF16>
 struct Raw {
     uint4 w[BF16 ? 1 : 2];
-    __device__ __forceinline__ void load(const void *x, int64_t i, bool on) {
-        const uint4 *const p = reinterpret_cast<const uint4 *>(static_cast<const char *>(x) + i * (BF16 ? 2 : 4));
+    __device__ __forceinline__ void load(const char *x, bool on) {
+        const uint4 *const p = reinterpret_cast<const uint4 *>(x);
 #pragma unroll
         for (int j = 0; j < (BF16 ? 1 : 2); ++j) w[j] = on ? __ldg(p + j) : make_uint4(0, 0, 0, 0);
     }
@@ -70,19 +72,20 @@ __device__ __forceinline__ void locate_tokens(const Kv4Cache &c, const Kv4Batch 
     __syncthreads();
 }
 
-// A lane's rows: one token, and of its 2 * heads rows (keys, then values) every step-th.
-template <int D>
+// A lane's rows: those of one token and side, heads first, first + step, ...  The token goes
+// fastest over the warps' rows, so that neighbouring rows of the cache are moved together.
+template <int D, int ITER>
 struct Rows {
-    static constexpr int LPR = D / 8, RP = 32 / LPR;
-    static_assert(kWarps * RP % kMaxTokens == 0, "a lane keeps its token");
     int tok, first, step;
+    bool side;  // values
     __device__ __forceinline__ Rows(int tokens_log2) {
-        const int r = blockIdx.y * kPerCta<D> + (threadIdx.x >> 5) * RP + (threadIdx.x & 31) / LPR;
+        const int warp = threadIdx.x >> 5;
+        const int r = blockIdx.y * (kSet<D> * ITER) + (warp & (kWarps / 2 - 1)) * (256 / D) + (threadIdx.x & 31) / (D / 8);
         tok = r & ((1 << tokens_log2) - 1);
         first = r >> tokens_log2;
-        step = (kWarps * RP) >> tokens_log2;
+        step = kSet<D> >> tokens_log2;
+        side = __shfl_sync(0xffffffffu, warp, 0) >= kWarps / 2;
     }
-    __device__ __forceinline__ int row(int it) const { return first + it * step; }
 };
 
 // A NaN in a row makes its step NaN, so that it is not lost.
@@ -93,7 +96,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 __device__ __forceinline__ float rcp(float x) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -111,39 +114,43 @@ template <bool BF16, int D, int BITS>
 __global__ void __launch_bounds__(32 * kWarps, BF16 ? 4 : 3)
 kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t T, int64_t kts, int64_t khs,
                  int64_t vts, int64_t vhs, Kv4Cache c, Kv4Batch bt, float eps, int tokens_log2, int *status) {
-    constexpr int LPR = D / 8;
+    constexpr int LPR = D / 8, kIter = kWriteIter;
     static_assert(kIter <= LPR, "lane i of a row keeps the step of iteration i");
     constexpr double kQ = BITS == 4 ? 2.6457513110645905905 : 3.0;
     constexpr float kZero = BITS == 4 ? 8.0f : 4.0f, kLevels = 2.0f * kZero - 1.0f;
-    __shared__ Place place[kMaxTokens];
+    __shared__ Place place[kMaxTokens<D>];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int lane = threadIdx.x & 31;
     const int p = lane % LPR;
     const int t0 = blockIdx.x << tokens_log2;
-    const Rows<D> id(tokens_log2);
+    const Rows<D, kIter> id(tokens_log2);
     const int heads = c.heads;
+    int live = 0;  // the lane's heads; lane 0 has the warp's most
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) live += id.first + it * id.step < heads;
+    const int most_live = __shfl_sync(0xffffffffu, live, 0);
     Raw<BF16> raw[kIter];
     {
-        const bool on = t0 + id.tok < T;
-        const int64_t from_k = (t0 + id.tok) * kts + 8 * p, from_v = (t0 + id.tok) * vts + 8 * p - heads * vhs;
+        constexpr int kSize = BF16 ? 2 : 4;
+        const int count = t0 + id.tok < T ? live : 0;
+        const int64_t hs = id.side ? vhs : khs;
+        const char *from = static_cast<const char *>(id.side ? v : k) + ((t0 + id.tok) * (id.side ? vts : kts) + id.first * hs + 8 * p) * kSize;
+        const int64_t stride = id.step * hs * kSize;
 #pragma unroll
-        for (int it = 0; it < kIter; ++it) {
-            const int hs = id.row(it);
-            const bool side = hs >= heads;
-            raw[it].load(side ? v : k, side ? from_v + hs * vhs : from_k + hs * khs, on && hs < 2 * heads);
-        }
+        for (int it = 0; it < kIter; ++it, from += stride) raw[it].load(from, it < count);
     }
     locate_tokens(c, bt, t0, 1 << tokens_log2, T, status, place);
     const Place at = place[id.tok];
-    const int64_t row0 = kv4_rows(c, max(at.page, 0), 0) + at.row;
+    const int64_t first = kv4_rows(c, max(at.page, 0), id.first) + at.row, stride = (int64_t)id.step << c.page_log2;
+    uint8_t *codes = (id.side ? c.v_codes : c.k_codes) + first * (D / 2) + 4 * p;
+    const int count = at.page >= 0 ? live : 0;
     const bool bos = at.pos == 0;
     float own = 0.0f;  // of iteration p: the scale, or the step where fp64 gave it
     bool is_step = false;
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-        const int hs = id.row(it);
-        if (__all_sync(0xffffffffu, hs >= 2 * heads)) break;
+    for (int it = 0; it < kIter; ++it, codes += stride * (D / 2)) {
+        if (it >= most_live) break;
         float x[8], a = 0.0f;
         raw[it].values(x);
 #pragma unroll
@@ -167,8 +174,6 @@ kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t
         const float hi = fmaf(fmaf(fmaf(f[7] + 2048.0f, 16.0f, f[6]), 16.0f, f[5]), 16.0f, f[4]);
         uint32_t w = (__byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410) + (BITS == 4 ? 0u : 0x44444444u)) ^ 0x88888888u;
         if (p == it) own = scale;
-        const bool live = at.page >= 0 && hs < 2 * heads, side = hs >= heads;
-        const int head = side ? hs - heads : hs;
         const uint32_t asks = __ballot_sync(0xffffffffu, bos || !(scale >= 1e-36f && scale <= 1e36f && most < 0.5f - 1.25e-6f * kZero));
         if (asks) {
             // the rows of a warp may differ in kind; every lane takes the same shuffles, and only
@@ -203,20 +208,15 @@ kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t
                     w |= (code & 15u) << (4 * e);
                     w8[e >> 2] |= (code & 255u) << (8 * (e & 3));
                 }
-                if (bos && live)
-                    *reinterpret_cast<uint2 *>((side ? c.v_bos : c.k_bos) + ((int64_t)at.page * heads + head) * D + 8 * p) =
+                if (bos && it < count)
+                    *reinterpret_cast<uint2 *>((id.side ? c.v_bos : c.k_bos) + ((int64_t)at.page * heads + id.first + it * id.step) * D + 8 * p) =
                         make_uint2(w8[0], w8[1]);
             }
         }
-        if (live)
-            *reinterpret_cast<uint32_t *>((side ? c.v_codes : c.k_codes) + (row0 + ((int64_t)head << c.page_log2)) * (D / 2) + 4 * p) = w;
+        if (it < count) *reinterpret_cast<uint32_t *>(codes) = w;
     }
-    const int hs = id.row(p);
-    if (p < kIter && hs < 2 * heads && at.page >= 0) {
-        const bool side = hs >= heads;
-        (side ? c.v_step : c.k_step)[row0 + ((int64_t)(side ? hs - heads : hs) << c.page_log2)] =
-            is_step ? own : __fdiv_rn(own, (float)kQ);
-    }
+    if (p < count)
+        (id.side ? c.v_step : c.k_step)[first + p * stride] = is_step ? own : __fdiv_rn(own, (float)kQ);
 }
 
 // Reading back: value = step * code.  Nibble e of a word plus 8, put into the mantissa of
@@ -227,48 +227,46 @@ template <bool BF16, int D>
 __global__ void __launch_bounds__(32 * kWarps)
 kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, void *__restrict__ v_out,
                 int tokens_log2, int *status) {
-    constexpr int LPR = D / 8;
-    __shared__ Place place[kMaxTokens];
+    constexpr int LPR = D / 8, kIter = kReadIter;
+    __shared__ Place place[kMaxTokens<D>];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int p = (threadIdx.x & 31) % LPR;
     const int t0 = blockIdx.x << tokens_log2;
-    const Rows<D> id(tokens_log2);
+    const Rows<D, kIter> id(tokens_log2);
     const int heads = c.heads;
     locate_tokens(c, bt, t0, 1 << tokens_log2, T, status, place);
     const Place at = place[id.tok];
-    if (at.pos == INT32_MIN) return;
+    void *const out = id.side ? v_out : k_out;
+    if (at.pos == INT32_MIN || !out) return;
     const bool on = at.page >= 0, bos = at.pos == 0;
-    const int64_t row0 = kv4_rows(c, max(at.page, 0), 0) + at.row;
+    const int64_t first = kv4_rows(c, max(at.page, 0), id.first) + at.row, stride = (int64_t)id.step << c.page_log2;
+    const uint8_t *const codes = (id.side ? c.v_codes : c.k_codes) + first * (D / 2);
+    const float *const steps = (id.side ? c.v_step : c.k_step) + first;
     uint32_t w[kIter];
     float step[kIter];
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-        const int hs = id.row(it);
-        const bool side = hs >= heads;
         w[it] = 0x88888888u, step[it] = 0.0f;
-        if (on && hs < 2 * heads) {
-            const int64_t row = row0 + ((int64_t)(side ? hs - heads : hs) << c.page_log2);
-            const uint8_t *const codes = (side ? c.v_codes : c.k_codes) + row * (D / 2);
-            step[it] = (side ? c.v_step : c.k_step)[row];
+        if (on && id.first + it * id.step < heads) {
+            const uint8_t *const from = codes + it * stride * (D / 2);
+            step[it] = steps[it * stride];
             if constexpr (BF16) {
-                w[it] = *reinterpret_cast<const uint32_t *>(codes + 4 * p);
+                w[it] = *reinterpret_cast<const uint32_t *>(from + 4 * p);
             } else {
-                const uint16_t *const c16 = reinterpret_cast<const uint16_t *>(codes) + p;
+                const uint16_t *const c16 = reinterpret_cast<const uint16_t *>(from) + p;
                 w[it] = c16[0] | (uint32_t)c16[LPR] << 16;
             }
         }
     }
+    const int64_t o = ((int64_t)(t0 + id.tok) * heads + id.first) * D + (BF16 ? 8 : 4) * p;
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-        const int hs = id.row(it);
-        const bool side = hs >= heads;
-        void *const out = side ? v_out : k_out;
-        if (hs >= 2 * heads || !out) continue;
-        const int head = side ? hs - heads : hs;
+        const int head = id.first + it * id.step;
+        if (head >= heads) break;
         float y[8];
         if (bos) {
-            const int8_t *const c8 = (side ? c.v_bos : c.k_bos) + ((int64_t)max(at.page, 0) * heads + head) * D;
+            const int8_t *const c8 = (id.side ? c.v_bos : c.k_bos) + ((int64_t)max(at.page, 0) * heads + head) * D;
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = on ? step[it] * (float)c8[BF16 ? 8 * p + e : 4 * p + (e & 3) + (e >> 2) * (D / 2)] : 0.0f;
         } else {
@@ -280,7 +278,6 @@ kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, vo
                 y[e] = step[it] * __fsub_rn(__uint_as_float((u[e >> 2] & (15u << (4 * (e & 3)))) | one), base);
             }
         }
-        const int64_t o = ((int64_t)(t0 + id.tok) * heads + head) * D;
         if constexpr (BF16) {
             uint32_t h[4];
 #pragma unroll
@@ -288,9 +285,9 @@ kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, vo
                 const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
                 h[e] = *reinterpret_cast<const uint32_t *>(&b);
             }
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + o + 8 * p) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + o + it * id.step * D) = make_uint4(h[0], h[1], h[2], h[3]);
         } else {
-            float *const d = reinterpret_cast<float *>(out) + o + 4 * p;
+            float *const d = reinterpret_cast<float *>(out) + o + it * id.step * D;
             *reinterpret_cast<float4 *>(d) = make_float4(y[0], y[1], y[2], y[3]);
             *reinterpret_cast<float4 *>(d + D / 2) = make_float4(y[4], y[5], y[6], y[7]);
         }
@@ -301,16 +298,16 @@ struct RowGrid {
     dim3 grid;
     int tokens_log2;
 };
-// Tokens of a CTA: four where that leaves at least eight CTAs to an SM (neighbouring rows
-// of the cache are then moved together), one otherwise.
-RowGrid row_grid(int64_t T, int heads, int D) {
+// Tokens of a CTA: as many as fill a CTA, and at least eight (neighbouring rows of the cache
+// are then moved together), as long as that leaves eight CTAs to an SM.
+RowGrid row_grid(int64_t T, int heads, int D, int iter) {
     RowGrid g;
-    const int per_round = kWarps * (256 / D) * kIter;
+    const int set = kWarps / 2 * (256 / D), per_cta = set * iter;
+    auto grid = [&](int log2) { return dim3((unsigned)ceil_div(T, 1 << log2), (unsigned)ceil_div((int64_t)heads << log2, per_cta)); };
     g.tokens_log2 = 0;
-    while (g.tokens_log2 < 2 && ceil_div(T, 2 << g.tokens_log2) * ceil_div((int64_t)2 * heads << (g.tokens_log2 + 1), per_round) >=
-                                    8 * (int64_t)sm_count())
-        ++g.tokens_log2;
-    g.grid = dim3((unsigned)ceil_div(T, 1 << g.tokens_log2), (unsigned)ceil_div((int64_t)2 * heads << g.tokens_log2, per_round));
+    for (int log2 = 1; (1 << log2) <= (set < 16 ? set : 16) && (log2 <= 3 || heads << log2 <= per_cta); ++log2)
+        if ((int64_t)grid(log2).x * grid(log2).y >= 8 * (int64_t)sm_count()) g.tokens_log2 = log2;
+    g.grid = grid(g.tokens_log2);
     return g;
 }
 
@@ -332,7 +329,7 @@ cudaError_t launch_rows(void (*kernel)(P...), dim3 grid, cudaStream_t s, A... ar
 
 cudaError_t launch_kv4_write(const void *k, const void *v, bool bf16, int64_t T, int64_t kts, int64_t khs, int64_t vts,
                              int64_t vhs, const Kv4Cache &c, const Kv4Batch &bt, int bits, float eps, cudaStream_t s) {
-    const RowGrid g = row_grid(T, c.heads, c.dim);
+    const RowGrid g = row_grid(T, c.heads, c.dim, kWriteIter);
     int *status = device_status_ptr();
     auto go = [&](auto kernel) { return launch_rows(kernel, g.grid, s, k, v, T, kts, khs, vts, vhs, c, bt, eps, g.tokens_log2, status); };
     auto of = [&](auto type, auto n) {
@@ -349,7 +346,7 @@ cudaError_t launch_kv4_write(const void *k, const void *v, bool bf16, int64_t T,
 
 cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &bt, int64_t T, void *k_out, void *v_out, bool bf16,
                             cudaStream_t s) {
-    const RowGrid g = row_grid(T, c.heads, c.dim);
+    const RowGrid g = row_grid(T, c.heads, c.dim, kReadIter);
     int *status = device_status_ptr();
     auto go = [&](auto kernel) {
         return launch_rows(kernel, g.grid, s, c, bt, T, k_out, v_out, g.tokens_log2, status);
