@@ -15,6 +15,7 @@ intermediate int8 codes, per-token scales and (optionally) the int32 accumulator
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -470,16 +471,23 @@ class KV4Cache:
 def _kv4_batch(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor):
     if not isinstance(cache, KV4Cache):
         raise TypeError("cache must be a KV4Cache")
-    B = kv_lens.shape[0] if isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1 else -1
-    _need(kv_lens, "kv_lens", torch.int32, (B,))
-    _need(q_starts, "q_starts", torch.int32, (B + 1,))
-    _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
     dev = cache.device
-    if block_table.device != dev or kv_lens.device != dev or q_starts.device != dev:
+    try:  # a step of a model makes these calls for each layer: one expression first, the reasons after it
+        B, width = block_table.shape
+        good = (kv_lens.shape == (B,) and q_starts.shape == (B + 1,) and
+                block_table.dtype is torch.int32 and kv_lens.dtype is torch.int32 and q_starts.dtype is torch.int32 and
+                block_table.device == dev and kv_lens.device == dev and q_starts.device == dev and
+                block_table.is_contiguous() and kv_lens.is_contiguous() and q_starts.is_contiguous())
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        B = kv_lens.shape[0] if isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1 else -1
+        _need(kv_lens, "kv_lens", torch.int32, (B,))
+        _need(q_starts, "q_starts", torch.int32, (B + 1,))
+        _need(block_table, "block_table", torch.int32)
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
         raise ValueError(f"block_table, kv_lens and q_starts must be on the cache's device {dev}")
-    width = block_table.shape[1]
     return _native.Kv4Batch(block_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr(), width, B, width)
 
 
@@ -487,25 +495,29 @@ def _rows(t: torch.Tensor, name: str, cache: KV4Cache, heads=None):
     """Checks a [T, heads, dim] tensor whose rows of dim lie anywhere; returns (T, token stride, head stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != cache.device:
+    if t.device != cache.device:
         raise ValueError(f"{name} must be a CUDA tensor on the cache's device {cache.device}")
-    if t.dim() != 3 or t.shape[2] != cache.dim or (heads is not None and t.shape[1] != heads):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != cache.dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have shape [T, {'heads' if heads is None else heads}, {cache.dim}], "
-                         f"got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+                         f"got {tuple(shape)}")
+    if stride[2] != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     # the stride of a dimension of one says nothing
-    return t.shape[0], t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    return shape[0], stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
 def _kv4_call(cache: KV4Cache, fn: str, stream, *args) -> None:
-    """The call with the cache's device current (a kernel is launched on the current one)."""
+    """The call with the cache's device current (a kernel is launched on the current one), on its current stream."""
     f = getattr(_native.load(), fn)
-    if cache.device.index == torch.cuda.current_device():
-        _native.check(fn, f(*args, _stream(stream)))
+    index = cache.device.index
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = f(*args, handle)
     else:
-        with torch.cuda.device(cache.device):
-            _native.check(fn, f(*args, _stream(stream)))
+        with torch.cuda.device(index):
+            status = f(*args, handle)
+    _native.check(fn, status)
 
 
 def bitnet_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor,
@@ -541,6 +553,7 @@ def bitnet_kv4_read(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.T
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=4096)
 def bitnet_kv4_attention_workspace_bytes(T: int, q_heads: int, heads: int, dim: int, batch: int) -> int:
     """Workspace of bitnet_kv4_attention for T rows of q_heads over a cache of `heads` key heads (0: sizes it refuses)."""
     return _native.load().bitnet_kv4_attention_workspace_bytes(T, q_heads, heads, dim, batch)
@@ -558,19 +571,22 @@ def bitnet_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Te
     run at the same time need workspaces of their own."""
     batch = _kv4_batch(cache, block_table, kv_lens, q_starts)
     T, qts, qhs = _rows(q, "q", cache)
-    dt, heads = _xdt(q), q.shape[1]
-    shape = (T, heads, cache.dim)
-    out = torch.empty(shape, dtype=q.dtype, device=cache.device) if out is None else out
-    _need(out, "out", q.dtype, shape)
-    if lse is None and return_lse:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
-    if lse is not None:
+    dt, heads, dev = _xdt(q), q.shape[1], cache.device
+    if out is None:
+        out = torch.empty((T, heads, cache.dim), dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", q.dtype, (T, heads, cache.dim))
+    if lse is None:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=dev) if return_lse else None
+    else:
         _need(lse, "lse", torch.float32, (T, heads))
-    nbytes = _native.load().bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch)
-    ws = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=cache.device) if ws is None else ws
-    _need(ws, "ws", torch.uint8)
-    if out.device != cache.device or ws.device != cache.device or (lse is not None and lse.device != cache.device):
-        raise ValueError(f"out, lse and ws must be on the cache's device {cache.device}")
+    if ws is None:
+        ws = torch.empty((bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch) or 256,),
+                         dtype=torch.uint8, device=dev)
+    else:
+        _need(ws, "ws", torch.uint8)
+    if out.device != dev or ws.device != dev or (lse is not None and lse.device != dev):
+        raise ValueError(f"out, lse and ws must be on the cache's device {dev}")
     scale = cache.dim ** -0.5 if scale is None else scale
     _kv4_call(cache, "bitnet_kv4_attention", stream, q.data_ptr(), dt, T, heads, qts, qhs, cache._ref,
               ctypes.byref(batch), scale, int(bool(causal)), window, max_q, out.data_ptr(),

@@ -101,7 +101,7 @@ bitnet_status_t bitnet_kv4_read(const bitnet_kv4_cache_t *cache, const bitnet_kv
 
 size_t bitnet_kv4_attention_workspace_bytes(int64_t T, int64_t q_heads, int64_t heads, int64_t dim, int64_t batch) {
     if (T <= 0 || T > kMaxTokens || heads < 1 || heads > kMaxHeads || q_heads < heads || q_heads > kMaxHeads ||
-        q_heads % heads != 0 || (dim != 64 && dim != 128 && dim != 256) || batch < 1 || batch > kMaxBatch)
+        q_heads % heads != 0 || T * q_heads > INT32_MAX || (dim != 64 && dim != 128 && dim != 256) || batch < 1 || batch > kMaxBatch)
         return 0;
     return kv4_attention_workspace(T, (int)q_heads, (int)heads, (int)dim, (int)batch);
 }
@@ -119,7 +119,8 @@ bitnet_status_t bitnet_kv4_attention(const void *q, bitnet_dtype_t dt, int64_t T
     bitnet_status_t st = shape_of(cache, &c);
     if (st == BITNET_OK) st = sizes_of(batch, T, &empty);
     if (st != BITNET_OK) return st;
-    if (q_heads < c.heads || q_heads > kMaxHeads || q_heads % c.heads != 0) return BITNET_ERR_UNSUPPORTED_SHAPE;
+    if (q_heads < c.heads || q_heads > kMaxHeads || q_heads % c.heads != 0 || T * q_heads > INT32_MAX)
+        return BITNET_ERR_UNSUPPORTED_SHAPE;
     if (empty) return BITNET_OK;
     if ((st = arrays_of(cache, batch, &b)) != BITNET_OK) return st;
     if (!valid_rows(q, dt, q_token_stride, q_head_stride) || !out || !aligned(out, 16) || !aligned(lse, 4))

@@ -78,8 +78,9 @@ struct RowsParams {
     int rows_max; // sequences with more rows (new tokens x group) are another kernel's
     void *out;
     float *lse;
-    float *part;  // [grid][2][8 NT][D + 2]: output, reference, sum
-    int4 *head;   // [grid]: {sequence, key head * row tiles + row tile, CTAs, 1 if this CTA's part is the second}
+    float *part;  // [grid][2]: outputs [8 NT][D], then reference and sum [8 NT][2]
+    int4 *head;   // [grid]: where this CTA's first part is the second of its item, {the sequence's first row among the
+                  // call's, the item's first row, its rows + 256 * key head, its parts}; no parts otherwise
     int *status;
     uint32_t magic[2];  // see halves()
 };
@@ -308,7 +309,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             const int64_t first = run0 - from;  // of the item
             if (!starts && W * (cta - 1) / G <= first) {
                 const int64_t last = ((first + unit) * G + W - 1) / W - 1;  // the first whose run ends behind the item
-                h = make_int4(b, item, (int)(last - cta + 2), 1);
+                h = make_int4(s.first, rt * R, min(R, s.rows - rt * R) + 256 * kh, (int)(last - cta + 2));
             }
             p.head[cta] = h;
         }
@@ -678,10 +679,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 y.x = fmaf(f, x.x, y.x), y.y = fmaf(f, x.y, y.y), y.z = fmaf(f, x.z, y.z), y.w = fmaf(f, x.w, y.w);
             }
             if (!whole) {
-                float *dst = part + n * (D + 2);
-                *reinterpret_cast<float2 *>(dst + d) = make_float2(y.x, y.y);
-                *reinterpret_cast<float2 *>(dst + d + 2) = make_float2(y.z, y.w);
-                if (d == 0) dst[D] = top, dst[D + 1] = sum;
+                *reinterpret_cast<float4 *>(part + n * D + d) = y;
+                if (d == 0) *reinterpret_cast<float2 *>(part + R * D + 2 * n) = make_float2(top, sum);
                 continue;
             }
             const int r = row0 + n, tok = r / p.group;
@@ -702,50 +701,75 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
 }
 
 // Joins the parts of the items that several CTAs of kv4_rows_kernel shared: one CTA to each of
-// that kernel's, which finds in p.head whether an item is its to join.
+// that kernel's, which finds in p.head whether an item is its to join.  A row is a warp's, or
+// several warps' where there are fewer rows than warps: each takes every so many-th part, and
+// their sums are added in order.  What it costs is the wait for the kernel before it and two
+// loads one after the other, the head and then everything else at a time.
 template <int D, int NT, bool BF16>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ RowsParams p) {
-    constexpr int R = 8 * NT;
-    constexpr int PER = D / 32;
+    constexpr int R = 8 * NT, W = 8;
+    constexpr int V = D / 32;  // values of a lane
+    __shared__ float so[W][D], sl[W];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int cta = blockIdx.x;
     const int4 h = p.head[cta];
-    if (h.w == 0) return;
+    const int parts = h.w;
+    if (parts == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Seq s = seq_of<R>(p, h.x);
-    const int kh = h.y / s.row_tiles, row0 = (h.y - kh * s.row_tiles) * R;
-    const int nrows = min(R, s.rows - row0);
-    const int q0 = s.first;
-    for (int n = warp; n < nrows; n += 8) {
-        // part 0 lies in the CTA before, as the one it began; the others continue it
-        auto part = [&](int i) { return p.part + (((int64_t)(cta - 1 + i) * 2 + (i == 0 ? 1 : 0)) * R + n) * (D + 2); };
-        float top = kNone;
-        for (int i = lane; i < h.z; i += 32) top = fmaxf(top, part(i)[D]);
+    const int nrows = h.z & 255, kh = h.z >> 8;
+    const int log2 = nrows > 4 ? 0 : (nrows > 2 ? 1 : (nrows > 1 ? 2 : 3));  // warps of a row
+    for (int n0 = 0; n0 < nrows; n0 += W >> log2) {
+        const int n = n0 + (warp >> log2);
+        float top = kNone, sum = 0.0f, y[V];
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        float sum = 0.0f, y[PER];
+        for (int e = 0; e < V; ++e) y[e] = 0.0f;
+        if (n < nrows) {
+            // part 0 lies in the CTA before, as the one it began; the others continue it
+            auto part = [&](int i) { return p.part + ((int64_t)(cta - 1 + i) * 2 + (i == 0 ? 1 : 0)) * (R * (D + 2)); };
+            for (int i = lane; i < parts; i += 32) top = fmaxf(top, part(i)[R * D + 2 * n]);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) y[e] = 0.0f;
+            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
 #pragma unroll 8
-        for (int i = 0; i < h.z; ++i) {
-            const float *x = part(i);
-            const float m = x[D], l = x[D + 1];
-            const float f = ex2(m - top);
-            sum = fmaf(f, l, sum);
+            for (int i = warp & ((1 << log2) - 1); i < parts; i += 1 << log2) {
+                const float *const x = part(i);
+                const float2 ml = *reinterpret_cast<const float2 *>(x + R * D + 2 * n);
+                const float f = ex2(ml.x - top);
+                sum = fmaf(f, ml.y, sum);
+                float v[V];
+                if constexpr (V == 2) {
+                    const float2 u = *reinterpret_cast<const float2 *>(x + n * D + 2 * lane);
+                    v[0] = u.x, v[1] = u.y;
+                } else {
 #pragma unroll
-            for (int e = 0; e < PER; e += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(x + lane * 2 + e * 32);
-                y[e] = fmaf(f, v.x, y[e]);
-                y[e + 1] = fmaf(f, v.y, y[e + 1]);
+                    for (int e = 0; e < V; e += 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(x + n * D + V * lane + e);
+                        v[e] = u.x, v[e + 1] = u.y, v[e + 2] = u.z, v[e + 3] = u.w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) y[e] = fmaf(f, v[e], y[e]);
             }
         }
-        const int r = row0 + n, tok = r / p.group;
-        const int64_t at = (int64_t)(q0 + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
+        if (log2 > 0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) so[warp][V * lane + e] = y[e];
+            if (lane == 0) sl[warp] = sum;
+            __syncthreads();
+            for (int w = 1; w < 1 << log2; ++w) {
+                const int from = min(W - 1, warp + w);
+                sum += sl[from];
+#pragma unroll
+                for (int e = 0; e < V; ++e) y[e] += so[from][V * lane + e];
+            }
+        }
+        if (n >= nrows || (warp & ((1 << log2) - 1)) != 0) continue;  // with several warps to a row this round is the only one
+        const int r = h.y + n, tok = r / p.group;
+        const int64_t at = (int64_t)(h.x + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) {
-            const int64_t d = at * D + lane * 2 + e * 32;
+        for (int e = 0; e < V; e += 2) {
+            const int64_t d = at * D + V * lane + e;
             if constexpr (BF16) *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + d) = h2_bf16(y[e] * inv, y[e + 1] * inv);
             else *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.out) + d) = make_float2(y[e] * inv, y[e + 1] * inv);
         }

@@ -92,6 +92,8 @@ def test_refused_attention(L):
         assert attend(L, **kw) == BAD, kw
     for heads in (0, 2, 6, 1 << 16, -4):
         assert attend(L, heads=heads) == SHAPE, heads
+    # rows of all heads are counted in 31 bits
+    assert attend(L, T=1 << 28) == SHAPE and L.bitnet_kv4_attention_workspace_bytes(1 << 28, 8, 4, 128, 2) == 0
     need = L.bitnet_kv4_attention_workspace_bytes(5, 8, 4, 128, 2)
     assert need > 0
     assert attend(L, ws=None, nws=0) == _native.ERR_WORKSPACE
