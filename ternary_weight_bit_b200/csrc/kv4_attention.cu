@@ -22,6 +22,7 @@ constexpr uint32_t kNowhere = 0xffffffffu;
 constexpr int kTile = 32;       // positions that a warp takes at a time
 constexpr int kMaxParts = 64;   // CTAs that may share an item on average
 constexpr int kMinTiles = 4;    // tiles that make a CTA of its own worth while
+constexpr int kJoinSplit = 2;   // CTAs that join an item, each some of its rows
 constexpr int kItemCost = 10;   // what beginning and ending an item takes, in tiles
 // Weights are held as 2^(s - m + kOff), and a score may pass the running maximum m by kLag before
 // that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
@@ -717,14 +718,16 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
     const int parts = h.w;
     if (parts == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nrows = h.z & 255, kh = h.z >> 8;
+    const int share = ((h.z & 255) + kJoinSplit - 1) / kJoinSplit, first = blockIdx.y * share;
+    const int nrows = min(share, (h.z & 255) - first), kh = h.z >> 8;
+    if (nrows <= 0) return;
     const int log2 = nrows > 4 ? 0 : (nrows > 2 ? 1 : (nrows > 1 ? 2 : 3));  // warps of a row
     for (int n0 = 0; n0 < nrows; n0 += W >> log2) {
-        const int n = n0 + (warp >> log2);
+        const int n = first + n0 + (warp >> log2);
         float top = kNone, sum = 0.0f, y[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] = 0.0f;
-        if (n < nrows) {
+        if (n < first + nrows) {
             // part 0 lies in the CTA before, as the one it began; the others continue it
             auto part = [&](int i) { return p.part + ((int64_t)(cta - 1 + i) * 2 + (i == 0 ? 1 : 0)) * (R * (D + 2)); };
             for (int i = lane; i < parts; i += 32) top = fmaxf(top, part(i)[R * D + 2 * n]);
@@ -763,7 +766,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
                 for (int e = 0; e < V; ++e) y[e] += so[from][V * lane + e];
             }
         }
-        if (n >= nrows || (warp & ((1 << log2) - 1)) != 0) continue;  // with several warps to a row this round is the only one
+        if (n >= first + nrows || (warp & ((1 << log2) - 1)) != 0) continue;  // with several warps to a row this round is the only one
         const int r = h.y + n, tok = r / p.group;
         const int64_t at = (int64_t)(h.x + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -778,9 +781,9 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_one(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_one(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -815,7 +818,7 @@ cudaError_t launch_rows(RowsParams p, int64_t T, void *ws, cudaStream_t s) {
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + (size_t)grid * sizeof(int4));
     const cudaError_t r = launch_one(kv4_rows_kernel<D, NT, BF16>, grid, 32 * kWarps, smem, s, p);
     if (r != cudaSuccess) return r;
-    return launch_one(kv4_join_kernel<D, NT, BF16>, grid, 256, 0, s, p);
+    return launch_one(kv4_join_kernel<D, NT, BF16>, dim3(grid, kJoinSplit), 256, 0, s, p);
 }
 
 }  // namespace
