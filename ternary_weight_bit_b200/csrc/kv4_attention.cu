@@ -23,7 +23,7 @@ constexpr int kTile = 32;       // positions that a warp takes at a time
 constexpr int kMaxParts = 64;   // CTAs that may share an item on average
 constexpr int kMinTiles = 4;    // tiles that make a CTA of its own worth while
 constexpr int kJoinSplit = 2;   // CTAs that join an item, each some of its rows
-constexpr int kItemCost = 10;   // what beginning and ending an item takes, in tiles
+constexpr int kItemCost = 16;   // what beginning and ending an item takes, in tiles
 // Weights are held as 2^(s - m + kOff), and a score may pass the running maximum m by kLag before
 // that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
 // for a finer second part.
@@ -48,23 +48,37 @@ __device__ __forceinline__ void each(F f) {  // f(constant 0), ..., f(constant N
     }
 }
 
-// A stage of a warp's ring: a tile's codes and steps, each lane's 16 (8, 4) bytes beside the others'.
+// A stage of a warp's ring: a tile's keys, values and steps, copied 16 bytes a lane as they lie
+// in the cache, but for an order of the chunks in which the lanes' loads meet no bank twice.
+// Lane (g, t) loads D / 8 bytes of key rows rk(g) + 8 n, rk = 4 (g % 2) + g / 2, at t, and D / 16
+// bytes of value rows t + 4 n at g.
 template <int D>
 struct Ring {
-    static constexpr uint32_t kKey = D / 8 * 32, kValue = D / 16 * 32;
-    static constexpr uint32_t kStage = 4 * kKey + 8 * kValue + 2 * 128;
-    static __host__ __device__ constexpr uint32_t key(int i) { return i * kKey; }
-    static __host__ __device__ constexpr uint32_t value(int i) { return 4 * kKey + i * kValue; }
-    static __host__ __device__ constexpr uint32_t step(int i) { return 4 * kKey + 8 * kValue + i * 128; }
+    static constexpr uint32_t kRow = D / 2, kChunks = D / 32, kBlock = 16 * kRow;  // a row, its chunks, a block of 16
+    static constexpr uint32_t kKeys = 0, kValues = 2 * kBlock, kSteps = 4 * kBlock;
+    static constexpr uint32_t kStage = kSteps + 2 * 4 * kTile;
+    // chunk c of row r, for the rows of a copy (of 512 / kRow rows)
+    static __device__ __forceinline__ uint32_t key(uint32_t r, uint32_t c) {
+        if constexpr (D == 64) return (r ^ (r >> 1 & 2)) * kRow + c * 16;
+        if constexpr (D == 128) return (r ^ (r >> 2 & 1)) * kRow + c * 16;
+        return r * kRow + (c ^ (r >> 2 & 1)) * 16;
+    }
+    static __device__ __forceinline__ uint32_t value(uint32_t r, uint32_t c) {
+        if constexpr (D == 64) return r * kRow + c * 16;
+        if constexpr (D == 128) return r * kRow + (c ^ (r & 2)) * 16;
+        return r * kRow + (c ^ (r & 3) * 2) * 16;
+    }
 };
 // Tiles of a warp under way at a time: what fits the shared memory of an SM with kResident CTAs.
-template <int D, int NT>
-constexpr int kResident = D == 64 && NT == 1 ? 3 : 2;
-template <int D, int NT>
-constexpr int kStages = D == 256 ? 3 : 5;
-template <int D, int NT>
-constexpr int kRowsSmem = (int)(kStages<D, NT> * Ring<D>::kStage) > 8 * NT * (D + 4) * 4 ? kWarps * (int)(kStages<D, NT> * Ring<D>::kStage)
-                                                                                      : kWarps * 8 * NT * (D + 4) * 4;
+// CTAs of an SM: three where their registers allow it (bf16, dim 128, 8 rows: 84 us for 64 sequences
+// of 256 to 8192 positions, against 88 with two).
+template <int D, int NT, bool BF16>
+constexpr int kResident = NT == 1 && (D == 64 || (D == 128 && BF16)) ? 3 : 2;
+template <int D, int NT, bool BF16>
+constexpr int kStages = D == 256 ? 3 : (D / 64 * kResident<D, NT, BF16> == 6 ? 4 : 5);
+template <int D, int NT, bool BF16>
+constexpr int kRowsSmem = kWarps * ((int)(kStages<D, NT, BF16> * Ring<D>::kStage) > 8 * NT * (D + 4) * 4 ? (int)(kStages<D, NT, BF16> * Ring<D>::kStage)
+                                                                                                        : 8 * NT * (D + 4) * 4);
 
 struct RowsParams {
     const void *q;
@@ -134,22 +148,14 @@ __device__ __forceinline__ void halves(uint32_t w, const uint32_t (&magic)[2], u
     h[3] = h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth, off16));
 }
 
-// A lane's copy of BYTES (4, 8 or a multiple of 16) into its own place in shared memory, dst + TO; zeros where
-// !on (nothing is read then).  Lanes stand min(BYTES, 16) apart, and each 16 bytes have a plane of their own.
-template <int BYTES, int TO, int FROM>
+// A lane's copy of 16 bytes into shared memory; zeros where !on (nothing is read then).
+template <int TO, int FROM>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t on) {
-    if constexpr (BYTES >= 16) {
-        asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, p;}" ::"r"(dst),
-                     "l"(src), "r"(on), "n"(TO), "n"(FROM)
-                     : "memory");
-        if constexpr (BYTES > 16) copy_async<BYTES - 16, TO + 512, FROM + 16>(dst, src, on);
-    } else {
-        asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.ca.shared.global [%0 + %3], [%1 + %4], %5, p;}" ::"r"(dst),
-                     "l"(src), "r"(on), "n"(TO), "n"(FROM), "n"(BYTES)
-                     : "memory");
-    }
+    asm volatile("{.reg .pred p; setp.eq.u32 p, %2, 0; cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, p;}" ::"r"(dst),
+                 "l"(src), "r"(on), "n"(TO), "n"(FROM)
+                 : "memory");
 }
-// What copy_async<BYTES, FROM, .> put there.
+// BYTES (4, 8 or 16) from shared memory.
 template <int BYTES, int FROM>
 __device__ __forceinline__ void take(uint32_t src, uint32_t *w) {
     if constexpr (BYTES == 4) {
@@ -161,7 +167,6 @@ __device__ __forceinline__ void take(uint32_t src, uint32_t *w) {
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(src), "n"(FROM)
                      : "memory");
-        if constexpr (BYTES > 16) take<BYTES - 16, FROM + 512>(src, w + 4);
     }
 }
 template <int N>
@@ -218,14 +223,14 @@ __device__ __forceinline__ int64_t weight(const RowsParams &p, const Seq &s) {
 // fp16 down to 2^-28 of the row's maximum.  fp32 calls carry queries and weights as the
 // sum of two fp16 numbers (22 bits).
 template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(32 * kWarps, kResident<D, NT>)
+__global__ void __launch_bounds__(32 * kWarps, kResident<D, NT, BF16>)
 kv4_rows_kernel(const __grid_constant__ RowsParams p) {
     constexpr int R = 8 * NT;
     constexpr int KW = D / 32;  // words of keys per lane and position
     constexpr int VW = D / 64;  // words of values per lane and position
     constexpr int NP = BF16 ? 1 : 2;
     constexpr int LD = D + 4;
-    extern __shared__ __align__(16) float so[];  // [kWarps][R][LD] once the loop is done, the warps' rings before
+    extern __shared__ __align__(128) float so[];  // [kWarps][R][LD] once the loop is done, the warps' rings before
     __shared__ float sm[kWarps][R], sl[kWarps][R];
     __shared__ int64_t scan[2 * kWarps];
     __shared__ int start_b;
@@ -235,7 +240,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
     pdl_wait_prerequisites();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_u32(so) + warp * (kStages<D, NT> * Ring<D>::kStage);
+    const uint32_t ring = smem_u32(so) + warp * (kStages<D, NT, BF16> * Ring<D>::kStage);
     const int B = p.bt.batch;
     const uint32_t magic[2] = {p.magic[0], p.magic[1]};
 
@@ -365,8 +370,11 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         uint32_t rows = rows_of(0, page0);
 
         const int rk = 4 * (g & 1) + (g >> 1);
-        const uint8_t *const k_base = p.c.k_codes + rk * (D / 2) + t * (D / 8);
-        const uint8_t *const v_base = p.c.v_codes + t * (D / 2) + g * (D / 16);
+        using S = Ring<D>;
+        const uint32_t row_in = lane / S::kChunks, chunk_in = lane % S::kChunks;
+        const uint32_t key_in = S::kKeys + S::key(row_in, chunk_in), value_in = S::kValues + S::value(row_in, chunk_in);
+        const uint8_t *const k_base = p.c.k_codes + lane * 16, *const v_base = p.c.v_codes + lane * 16;
+        const float *const step_base = (lane & 8 ? p.c.v_step : p.c.k_step) + (lane & 3) * 4;
         uint32_t valid = 0;  // two bits for each tile under way: whether its blocks lie somewhere
         auto fetch = [&](int i, uint32_t slot) {  // the copies of the warp's tile i; one group, empty past the end
             valid <<= 2;
@@ -376,31 +384,35 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                     pages = page_of(i + 16);
                 }
                 uint32_t r[2];
-                const uint32_t to_k = slot + lane * min(D / 8, 16), to_v = slot + lane * min(D / 16, 16);
+                const uint32_t to_k = slot + key_in, to_v = slot + value_in;
                 each<2>([&](auto h) {
                     r[h] = __shfl_sync(0xffffffffu, rows, 2 * (i & 15) + h);
                     const uint32_t on = r[h] != kNowhere;
                     valid |= on << h;
-                    const uint64_t off = (uint64_t)(on ? r[h] : 0) * (D / 2);
+                    const uint64_t off = (uint64_t)(on ? r[h] : 0) * S::kRow;
                     const uint8_t *const k = k_base + off, *const v = v_base + off;
-                    each<2>([&](auto e) { copy_async<D / 8, Ring<D>::key(2 * h + e), e * 8 * (D / 2)>(to_k, k, on); });
-                    each<4>([&](auto e) { copy_async<D / 16, Ring<D>::value(4 * h + e), e * 4 * (D / 2)>(to_v, v, on); });
+                    each<D / 64>([&](auto e) {
+                        // of dim 256, every other copy has the rows 4 .. 7 of 8
+                        copy_async<h * S::kBlock + e * 512, e * 512>(D == 256 && (e & 1) ? to_k ^ 16 : to_k, k, on);
+                        copy_async<h * S::kBlock + e * 512, e * 512>(to_v, v, on);
+                    });
                 });
-                const uint32_t own = lane < 16 ? r[0] : r[1];
+                // lanes 0 .. 7 bring the key steps, 8 .. 15 the value steps
+                const uint32_t own = lane & 4 ? r[1] : r[0];
                 const uint32_t on = own != kNowhere;
-                const uint32_t at = on ? own + (lane & 15) : 0;
-                copy_async<4, Ring<D>::step(0), 0>(slot + lane * 4, p.c.k_step + at, on);
-                copy_async<4, Ring<D>::step(1), 0>(slot + lane * 4, p.c.v_step + at, on);
+                if (lane < 16) copy_async<S::kSteps, 0>(slot + lane * 16, step_base + (on ? own : 0), on);
             }
             copies_commit();
         };
+        const uint32_t key_out = S::kKeys + S::key(rk, t * (D / 8) / 16) + t * (D / 8) % 16;
+        const uint32_t value_out = S::kValues + S::value(t, g * (D / 16) / 16) + g * (D / 16) % 16;
         uint32_t slot_in = ring, slot_out = ring;
         auto advance = [&](uint32_t &slot) {
             slot += Ring<D>::kStage;
-            if (slot == ring + kStages<D, NT> * Ring<D>::kStage) slot = ring;
+            if (slot == ring + kStages<D, NT, BF16> * Ring<D>::kStage) slot = ring;
         };
 #pragma unroll
-        for (int i = 0; i < kStages<D, NT> - 1; ++i) {
+        for (int i = 0; i < kStages<D, NT, BF16> - 1; ++i) {
             fetch(i, slot_in);
             advance(slot_in);
         }
@@ -492,17 +504,19 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
 
         for (int it = 0; it < count; ++it) {
             const int at = (tile0 + lo + warp + it * kWarps) * kTile;
-            fetch(it + kStages<D, NT> - 1, slot_in);
+            fetch(it + kStages<D, NT, BF16> - 1, slot_in);
             advance(slot_in);
-            copies_wait<kStages<D, NT> - 1>();
+            copies_wait<kStages<D, NT, BF16> - 1>();
 
             // S = K Q^T
             float sc[NT][2][4];
-            const uint32_t from_k = slot_out + lane * min(D / 8, 16), from_v = slot_out + lane * min(D / 16, 16);
+            const uint32_t from_k = slot_out + key_out, from_v = slot_out + value_out;
             each<2>([&](auto h) {
                 uint32_t kw[2][KW];
-                take<D / 8, Ring<D>::key(2 * h)>(from_k, kw[0]);
-                take<D / 8, Ring<D>::key(2 * h + 1)>(from_k, kw[1]);
+                each<2>([&](auto e) {
+                    take<(D < 256 ? D / 8 : 16), h * S::kBlock + 8 * e * S::kRow>(from_k, kw[e]);
+                    if constexpr (D == 256) take<16, h * S::kBlock + 8 * e * S::kRow>(from_k ^ 16, kw[e] + 4);
+                });
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     uint32_t x[4], y[4];
@@ -524,9 +538,9 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             // no step of the tile is twice as large as
             const int own = at + lane;
             uint32_t steps[2];
-            take<4, Ring<D>::step(0)>(slot_out + lane * 4, &steps[0]);
-            take<4, Ring<D>::step(1)>(slot_out + lane * 4, &steps[1]);
-            const bool live = own >= max(begin, 1) && own < end && (valid >> (2 * (kStages<D, NT> - 1) + (lane >> 4)) & 1);
+            take<4, S::kSteps>(slot_out + lane * 4, &steps[0]);
+            take<4, S::kSteps + 4 * kTile>(slot_out + lane * 4, &steps[1]);
+            const bool live = own >= max(begin, 1) && own < end && (valid >> (2 * (kStages<D, NT, BF16> - 1) + (lane >> 4)) & 1);
             const uint32_t vbits = live ? steps[1] & 0x7f800000u : 0u;
             const bool bad = vbits == 0x7f800000u;  // a value step that is not finite: NaN for the rows that see it, and for no others
             const float kstep = bad ? CUDART_NAN_F : (live ? __uint_as_float(steps[0]) : 0.0f);
@@ -611,7 +625,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 }
             // O = O + V^T P
             uint32_t vw[8][VW];
-            each<8>([&](auto i) { take<D / 16, Ring<D>::value(i)>(from_v, vw[i]); });
+            each<8>([&](auto i) { take<D / 16, 4 * i * S::kRow>(from_v, vw[i]); });
 #pragma unroll
             for (int j = 0; j < VW; ++j)
 #pragma unroll
@@ -808,11 +822,11 @@ cudaError_t allow_smem(const void *kernel, int bytes, bool (&done)[kMaxDevices])
 
 template <int D, int NT, bool BF16>
 cudaError_t launch_rows(RowsParams p, int64_t T, void *ws, cudaStream_t s) {
-    constexpr size_t smem = kRowsSmem<D, NT>;
+    constexpr size_t smem = kRowsSmem<D, NT, BF16>;
     static bool allowed[kMaxDevices] = {};
     const cudaError_t e = allow_smem((const void *)kv4_rows_kernel<D, NT, BF16>, (int)smem, allowed);
     if (e != cudaSuccess) return e;
-    const int slots = sm_count() * kResident<D, NT>;
+    const int slots = sm_count() * kResident<D, NT, BF16>;
     const int grid = slots;
     p.head = static_cast<int4 *>(ws);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + (size_t)grid * sizeof(int4));
@@ -824,12 +838,12 @@ cudaError_t launch_rows(RowsParams p, int64_t T, void *ws, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_attention_workspace(int64_t T, int q_heads, int heads, int dim, int batch) {
-    // the largest of the kernels': a slot and two parts of 8 NT rows to a CTA
+    // the largest of the kernels' (fp32 has no more CTAs than bf16): a slot and two parts of 8 NT rows to a CTA
     auto need = [&](int resident, int nt) {
         return (size_t)sm_count() * resident * (sizeof(int4) + 2 * 8 * nt * (size_t)(dim + 2) * 4);
     };
-    const size_t one = dim == 64 ? need(kResident<64, 1>, 1) : (dim == 128 ? need(kResident<128, 1>, 1) : need(kResident<256, 1>, 1));
-    const size_t two = dim == 64 ? need(kResident<64, 2>, 2) : (dim == 128 ? need(kResident<128, 2>, 2) : 0);
+    const size_t one = dim == 64 ? need(kResident<64, 1, true>, 1) : (dim == 128 ? need(kResident<128, 1, true>, 1) : need(kResident<256, 1, true>, 1));
+    const size_t two = dim == 64 ? need(kResident<64, 2, true>, 2) : (dim == 128 ? need(kResident<128, 2, true>, 2) : 0);
     // the kernels run one after the other in the same memory
     const int64_t rows = T * (q_heads / heads);
     const size_t tiles = dim <= 128 && rows >= kTilesFrom ? kv4_tiles_workspace(T, q_heads / heads, heads, dim, batch, kTilesFrom) : 0;
