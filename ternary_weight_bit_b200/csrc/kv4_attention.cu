@@ -23,6 +23,11 @@ constexpr int kTile = 32;       // positions that a warp takes at a time
 constexpr int kMaxParts = 64;   // CTAs that may share an item on average
 constexpr int kMinTiles = 4;    // tiles that make a CTA of its own worth while
 constexpr int kJoinSplit = 2;   // CTAs that join an item, each some of its rows
+// Items that can have no more tiles than this are not shared between CTAs (then there is nothing to join), and twice as
+// many where there are items for every CTA.  Measured in a graph (whole, shared) at 8 key heads of dim 128: 64
+// sequences of 500 positions 27 and 33 us, of 1000 39 and 44; one of 500 11 and 9, but its call takes 15.6 and
+// 17.8, which the host's second launch bounds; one of 1000 16 and 9.
+constexpr int kWholeTiles = 16;
 constexpr int kItemCost = 16;   // what beginning and ending an item takes, in tiles
 // Weights are held as 2^(s - m + kOff), and a score may pass the running maximum m by kLag before
 // that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
@@ -90,6 +95,7 @@ struct RowsParams {
     float scale;
     int causal;
     int window;   // INT32_MAX: none
+    int whole;    // every item is one CTA's, and there is no kernel to join parts
     int rows_max; // sequences with more rows (new tokens x group) are another kernel's
     void *out;
     float *lse;
@@ -200,8 +206,9 @@ __device__ __forceinline__ Seq seq_of(const RowsParams &p, int b) {
     if (s.cap < len && s.rows > 0) record_status(p.status, (int)BITNET_ERR_INVALID_ARG);
     return s;
 }
+__device__ __forceinline__ int unit_of(const RowsParams &p, const Seq &s) { return p.whole ? 1 : s.tiles + kItemCost; }
 __device__ __forceinline__ int64_t weight(const RowsParams &p, const Seq &s) {
-    return (int64_t)s.row_tiles * p.c.heads * (s.tiles + kItemCost);
+    return (int64_t)s.row_tiles * p.c.heads * unit_of(p, s);
 }
 
 // Every CTA takes an equal run of all tiles of all items, in order; the run's first and last
@@ -273,7 +280,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         items += scan[kWarps + w];
     }
     int64_t G = gridDim.x;
-    G = max((int64_t)1, min(min(G, items * kMaxParts), (W + kMinTiles - 1) / kMinTiles));
+    G = max((int64_t)1, p.whole ? min(G, W) : min(min(G, items * kMaxParts), (W + kMinTiles - 1) / kMinTiles));
     const int64_t cta = blockIdx.x;
     const int64_t run0 = cta < G ? W * cta / G : W, run_end = cta < G ? W * (cta + 1) / G : W;
     if (run0 >= run_end) {
@@ -303,12 +310,12 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             off -= weight(p, s);
             s = seq_of<R>(p, ++b);
         }
-        const int unit = s.tiles + kItemCost;
+        const int unit = unit_of(p, s);
         const int item = (int)(off / unit);  // key head * row tiles + row tile
         const int kh = item / s.row_tiles, rt = item - kh * s.row_tiles;
         const int from = (int)(off - (int64_t)item * unit), to = (int)min((int64_t)unit, from + (run_end - run));
         const bool starts = from == 0, whole = starts && to == unit;
-        const int lo = max(0, from - kItemCost), hi = max(0, to - kItemCost);  // tiles
+        const int lo = p.whole ? 0 : max(0, from - kItemCost), hi = p.whole ? s.tiles : max(0, to - kItemCost);  // tiles
         if (run == run0 && tid == 0) {
             // where this CTA's first part is the second of its item, it names the CTAs that share the item
             int4 h = make_int4(0, 0, 0, 0);
@@ -831,7 +838,7 @@ cudaError_t launch_rows(RowsParams p, int64_t T, void *ws, cudaStream_t s) {
     p.head = static_cast<int4 *>(ws);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + (size_t)grid * sizeof(int4));
     const cudaError_t r = launch_one(kv4_rows_kernel<D, NT, BF16>, grid, 32 * kWarps, smem, s, p);
-    if (r != cudaSuccess) return r;
+    if (r != cudaSuccess || p.whole) return r;
     return launch_one(kv4_join_kernel<D, NT, BF16>, dim3(grid, kJoinSplit), 256, 0, s, p);
 }
 
@@ -865,6 +872,8 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
     const bool tiles = bf16 && c.dim <= 128 && rows >= kTilesFrom;
     p.rows_max = tiles ? kTilesFrom - 1 : INT32_MAX;
     p.out = out, p.lse = lse, p.status = device_status_ptr();
+    const bool many = (int64_t)bt.batch * c.heads >= 2 * sm_count();
+    p.whole = ((int64_t)bt.max_pages << c.page_log2) <= (many ? 2 : 1) * kWholeTiles * kTile;
     p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
     if (tiles) {
         const cudaError_t e = launch_kv4_tiles(q, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, ws, s);
