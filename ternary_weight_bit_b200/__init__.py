@@ -507,6 +507,15 @@ def _rows(t: torch.Tensor, name: str, cache: KV4Cache, heads=None):
     return shape[0], stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
+def _empty(shape, dtype, cache: KV4Cache, stream) -> torch.Tensor:
+    """Memory for a call on `stream`, from that stream's pool: no other stream's work still uses it, or will before
+    the call is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+
+
 def _kv4_call(cache: KV4Cache, fn: str, stream, *args) -> None:
     """The call with the cache's device current (a kernel is launched on the current one), on its current stream."""
     f = getattr(_native.load(), fn)
@@ -542,8 +551,8 @@ def bitnet_kv4_read(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.T
     batch = _kv4_batch(cache, block_table, kv_lens, q_starts)
     dt = _out_dt(dtype)
     shape = (total, cache.heads, cache.dim)
-    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
+    k_out = _empty(shape, dtype, cache, stream) if k_out is None else k_out
+    v_out = _empty(shape, dtype, cache, stream) if v_out is None else v_out
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         _need(t, name, dtype, shape)
         if t.device != cache.device:
@@ -573,16 +582,16 @@ def bitnet_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Te
     T, qts, qhs = _rows(q, "q", cache)
     dt, heads, dev = _xdt(q), q.shape[1], cache.device
     if out is None:
-        out = torch.empty((T, heads, cache.dim), dtype=q.dtype, device=dev)
+        out = _empty((T, heads, cache.dim), q.dtype, cache, stream)
     else:
         _need(out, "out", q.dtype, (T, heads, cache.dim))
     if lse is None:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=dev) if return_lse else None
+        lse = _empty((T, heads), torch.float32, cache, stream) if return_lse else None
     else:
         _need(lse, "lse", torch.float32, (T, heads))
     if ws is None:
-        ws = torch.empty((bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch) or 256,),
-                         dtype=torch.uint8, device=dev)
+        ws = _empty((bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch) or 256,),
+                    torch.uint8, cache, stream)
     else:
         _need(ws, "ws", torch.uint8)
     if out.device != dev or ws.device != dev or (lse is not None and lse.device != dev):

@@ -510,6 +510,21 @@ def test_streams_and_captured_graphs():
         lens += 1  # the graph follows the lengths; every last page has room
 
 
+def test_memory_of_a_call_comes_from_its_stream(monkeypatch):
+    batch = Batch([300, 40], [1, 3], 64, seed=5)
+    c, _ = filled(batch, 2, 64, 64, seed=5)
+    q = queries(4, 4, 64, "bf16", seed=5)
+    tensors = batch.tensors(DEV)
+    want = tb.bitnet_kv4_attention(q, c, *tensors, return_lse=True) + tb.bitnet_kv4_read(c, *tensors, 4)
+    torch.cuda.synchronize()
+    side, seen, empty = torch.cuda.Stream(), [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: seen.append(torch.cuda.current_stream()) or empty(*a, **kw))
+    got = tb.bitnet_kv4_attention(q, c, *tensors, return_lse=True, stream=side) + tb.bitnet_kv4_read(c, *tensors, 4, stream=side)
+    assert len(seen) == 5 and all(s == side for s in seen)  # out, lse, workspace; keys, values
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_no_rows_and_no_sequences():
     batch = Batch([5], [0], 16)
     c, _ = filled(batch, 1, 64, 16)
@@ -535,6 +550,18 @@ def test_many_sequences():
     q = queries(batch.rows, 4, 64, "bf16")
     out, lse = run_attention(batch, c, q, max_q=1)
     check_attention(batch, c, held, q, out, lse, 64 ** -0.5, True, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("width", [8, 9, 16, 17, 90])  # whether items are shared between CTAs goes by the table's width
+def test_short_contexts_with_narrow_and_wide_tables(width, dtype):
+    lens = [(61 * i) % 500 + 3 for i in range(50)]
+    for sequences in (2, 50):
+        batch = Batch(lens[:sequences], [1 + i % 3 for i in range(sequences)], 64, width=width)
+        c, held = filled(batch, 8, 128, 64)
+        q = queries(batch.rows, 8, 128, dtype)
+        out, lse = run_attention(batch, c, q, max_q=3)
+        check_attention(batch, c, held, q, out, lse, 128 ** -0.5, True, 0)
 
 
 # ------------------------------------------------------------------ together, as a layer uses them
