@@ -349,7 +349,8 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *                     sequence whose first page this is (its step is in k_step and
  *                     v_step, row 0; its 4-bit row is not read).
  *   page_size is 16, 32, 64, 128 or 256; dim is 64, 128 or 256; heads is the number of
- *   key heads (BITNET_ERR_UNSUPPORTED_SHAPE otherwise).
+ *   key heads, at most 32768; pages * heads * page_size is below 2^32 - 64
+ *   (BITNET_ERR_UNSUPPORTED_SHAPE otherwise).
  *   Nothing needs initialising: rows that no write has reached are never read.
  *
  * bitnet_kv4_batch_t: the batch a call works on, device arrays of int32.
@@ -394,15 +395,18 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *   A row that sees no position gives out = 0 and lse = -infinity.
  *   q        [T][q_heads][dim] fp32 or bf16 (dt), strides as above.
  *   out      [T][q_heads][dim] of dt, densely packed;  lse [T][q_heads] fp32 or NULL.
- *   q_heads  a multiple of heads.  window >= 0, and 0 unless causal.
+ *   q_heads  a multiple of heads, at most 32768, with T * q_heads < 2^31
+ *            (BITNET_ERR_UNSUPPORTED_SHAPE).  window >= 0, and 0 unless causal.
  *   max_q    0, or the largest n_b of the batch where the caller knows it (a hint for
  *            the choice of kernel; results stay right where it is wrong).
  *   ws       device scratch of at least bitnet_kv4_attention_workspace_bytes(...) bytes
  *            (256-byte aligned; BITNET_ERR_WORKSPACE if smaller).  Its contents need no
- *            initialisation.
+ *            initialisation.  Calls that may run at the same time need one each.
  *   Products and sums are fp32 (codes and scaled queries enter the tensor cores exactly in bf16
  *   calls; fp32 calls split queries and probabilities into two fp16 parts); sums run in a fixed
- *   order, so equal calls give equal bits.  scale must be finite.
+ *   order, so equal calls give equal bits (other T, batch or tables may divide the sums
+ *   in other ways).  scale must be finite.  A weight times its value's step is rounded to 11 bits
+ *   (fp32 calls: 22), but no finer than to 2^-28 (2^-38) of the row's largest weight.  A row that sees a step or a query that is not finite is NaN; other rows are not touched by it.
  * ------------------------------------------------------------------------ */
 typedef struct {
     uint8_t *k_codes, *v_codes;
@@ -470,7 +474,8 @@ BITNET_API bitnet_status_t bitnet_gemm_force_k_splits(int k_splits);
  * Status and diagnostics (no counterpart on the pages).
  * bitnet_status_string: static English text for a status code.
  * bitnet_get_last_device_status: synchronises `stream`, returns the status word
- *   the kernels record on a bounded-wait timeout (BITNET_OK if none) and clears it.
+ *   the kernels record on a bounded-wait timeout, or on a page number or a length that
+ *   the 4-bit cache cannot serve (BITNET_OK if none), and clears it.
  * bitnet_selftest_wait_timeout: launches one CTA that waits on a barrier nothing
  *   will ever complete, with the given limit in microseconds (1..1000000); the
  *   wait gives up, records BITNET_ERR_TIMEOUT and the kernel returns normally.

@@ -224,7 +224,7 @@ __device__ __forceinline__ int64_t weight(const RowsParams &p, const Seq &s) {
 //
 // Scores stand in units of log2.  The running maximum m of a row moves only when a score
 // passes it by more than kLag, so most tiles have no reduction and no rescaling; weights
-// 2^(s - m + kOff) stay below 2^15 and keep fp16's eleven bits down to 2^-21 of the maximum.
+// 2^(s - m + kOff) stay below 2^15 and keep fp16's eleven bits down to 2^-17 of the maximum.
 // A tile's value steps are divided by their maximum, which scales the tile's product in fp32.
 // Queries are scaled by a power of two into [2^14, 2^15); bf16 queries are then exact in
 // fp16 down to 2^-28 of the row's maximum.  fp32 calls carry queries and weights as the
@@ -737,11 +737,12 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
     const int cta = blockIdx.x;
     const int4 h = p.head[cta];
     const int parts = h.w;
-    if (parts == 0) return;
+    // (A workspace that calls share at the same time can hold anything; what is no item's is left alone.)
+    if (parts <= 0 || cta == 0 || parts > (int)gridDim.x - cta + 1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int share = ((h.z & 255) + kJoinSplit - 1) / kJoinSplit, first = blockIdx.y * share;
     const int nrows = min(share, (h.z & 255) - first), kh = h.z >> 8;
-    if (nrows <= 0) return;
+    if (nrows <= 0 || nrows > R || (unsigned)kh >= (unsigned)p.c.heads || h.x < 0 || h.y < 0) return;
     const int log2 = nrows > 4 ? 0 : (nrows > 2 ? 1 : (nrows > 1 ? 2 : 3));  // warps of a row
     for (int n0 = 0; n0 < nrows; n0 += W >> log2) {
         const int n = first + n0 + (warp >> log2);
@@ -789,7 +790,8 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
         }
         if (n >= first + nrows || (warp & ((1 << log2) - 1)) != 0) continue;  // with several warps to a row this round is the only one
         const int r = h.y + n, tok = r / p.group;
-        const int64_t at = (int64_t)(h.x + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
+        if ((int64_t)h.x + tok >= p.T) continue;
+        const int64_t at = ((int64_t)h.x + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
         for (int e = 0; e < V; e += 2) {

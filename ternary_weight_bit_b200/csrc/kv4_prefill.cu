@@ -761,7 +761,8 @@ __global__ void __launch_bounds__(256) kv4_tiles_join_kernel(const __grid_consta
     const int item = blockIdx.x >> 3, row = (blockIdx.x & 7) * 32 + lane;
     const float *const src = p.part + (int64_t)item * p.splits * (D + 2) * (2 * kRows) + row;
     constexpr int64_t kPart = (D + 2) * (2 * kRows);
-    const int64_t place = p.place[(int64_t)item * (2 * kRows) + row];
+    int64_t place = p.place[(int64_t)item * (2 * kRows) + row];
+    if (place >= p.T * p.q_heads) place = -1;  // a workspace that calls share at the same time can hold anything
     if (__syncthreads_and(place < 0)) return;  // nobody's rows, whose parts may not be written
     float top = kNone, sum = 0.0f;
     for (int s = 0; s < p.splits; ++s) top = fmaxf(top, src[s * kPart + D * (2 * kRows)]);
