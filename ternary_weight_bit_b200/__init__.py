@@ -507,26 +507,26 @@ def _rows(t: torch.Tensor, name: str, cache: KV4Cache, heads=None):
     return shape[0], stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
-def _empty(shape, dtype, cache: KV4Cache, stream) -> torch.Tensor:
-    """Memory for a call on `stream`, from that stream's pool: no other stream's work still uses it, or will before
-    the call is done with it."""
+def _empty(like: torch.Tensor, shape, stream, dtype=None) -> torch.Tensor:
+    """Memory for a call on `stream`, of the type (unless given) and device of `like`, from that stream's pool: no other
+    stream's work still uses it, or will before the call is done with it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=cache.device)
+        return like.new_empty(shape, dtype=dtype) if dtype else like.new_empty(*shape)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=cache.device)
+        return like.new_empty(shape, dtype=dtype or like.dtype)
 
 
 def _kv4_call(cache: KV4Cache, fn: str, stream, *args) -> None:
     """The call with the cache's device current (a kernel is launched on the current one), on its current stream."""
-    f = getattr(_native.load(), fn)
     index = cache.device.index
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch.cuda.current_device():
-        status = f(*args, handle)
+        status = getattr(_native.load(), fn)(*args, handle)
     else:
         with torch.cuda.device(index):
-            status = f(*args, handle)
-    _native.check(fn, status)
+            status = getattr(_native.load(), fn)(*args, handle)
+    if status:
+        _native.check(fn, status)
 
 
 def bitnet_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor,
@@ -551,12 +551,13 @@ def bitnet_kv4_read(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.T
     batch = _kv4_batch(cache, block_table, kv_lens, q_starts)
     dt = _out_dt(dtype)
     shape = (total, cache.heads, cache.dim)
-    k_out = _empty(shape, dtype, cache, stream) if k_out is None else k_out
-    v_out = _empty(shape, dtype, cache, stream) if v_out is None else v_out
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _need(t, name, dtype, shape)
-        if t.device != cache.device:
-            raise ValueError(f"{name} must be on the cache's device {cache.device}")
+        if t is not None:
+            _need(t, name, dtype, shape)
+            if t.device != cache.device:
+                raise ValueError(f"{name} must be on the cache's device {cache.device}")
+    k_out = _empty(cache.k_step, shape, stream, dtype) if k_out is None else k_out
+    v_out = _empty(cache.k_step, shape, stream, dtype) if v_out is None else v_out
     _kv4_call(cache, "bitnet_kv4_read", stream, cache._ref, ctypes.byref(batch), total, k_out.data_ptr(),
               v_out.data_ptr(), dt)
     return k_out, v_out
@@ -582,16 +583,16 @@ def bitnet_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Te
     T, qts, qhs = _rows(q, "q", cache)
     dt, heads, dev = _xdt(q), q.shape[1], cache.device
     if out is None:
-        out = _empty((T, heads, cache.dim), q.dtype, cache, stream)
+        out = _empty(q, (T, heads, cache.dim), stream)
     else:
         _need(out, "out", q.dtype, (T, heads, cache.dim))
     if lse is None:
-        lse = _empty((T, heads), torch.float32, cache, stream) if return_lse else None
+        lse = _empty(cache.k_step, (T, heads), stream) if return_lse else None
     else:
         _need(lse, "lse", torch.float32, (T, heads))
     if ws is None:
-        ws = _empty((bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch) or 256,),
-                    torch.uint8, cache, stream)
+        ws = _empty(cache.k_codes,
+                    (bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch) or 256,), stream)
     else:
         _need(ws, "ws", torch.uint8)
     if out.device != dev or ws.device != dev or (lse is not None and lse.device != dev):

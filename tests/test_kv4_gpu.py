@@ -510,17 +510,20 @@ def test_streams_and_captured_graphs():
         lens += 1  # the graph follows the lengths; every last page has room
 
 
-def test_memory_of_a_call_comes_from_its_stream(monkeypatch):
+def test_memory_of_a_call_comes_from_its_stream():
     batch = Batch([300, 40], [1, 3], 64, seed=5)
     c, _ = filled(batch, 2, 64, 64, seed=5)
     q = queries(4, 4, 64, "bf16", seed=5)
     tensors = batch.tensors(DEV)
     want = tb.bitnet_kv4_attention(q, c, *tensors, return_lse=True) + tb.bitnet_kv4_read(c, *tensors, 4)
     torch.cuda.synchronize()
-    side, seen, empty = torch.cuda.Stream(), [], torch.empty
-    monkeypatch.setattr(torch, "empty", lambda *a, **kw: seen.append(torch.cuda.current_stream()) or empty(*a, **kw))
+    side = torch.cuda.Stream()
+    torch.cuda.memory._record_memory_history(context=None, max_entries=100)
     got = tb.bitnet_kv4_attention(q, c, *tensors, return_lse=True, stream=side) + tb.bitnet_kv4_read(c, *tensors, 4, stream=side)
-    assert len(seen) == 5 and all(s == side for s in seen)  # out, lse, workspace; keys, values
+    traces = torch.cuda.memory._snapshot()["device_traces"][torch.cuda.current_device()]
+    torch.cuda.memory._record_memory_history(enabled=None)
+    streams = [e["stream"] for e in traces if e["action"] == "alloc"]
+    assert streams == [side.cuda_stream] * 5  # output, sums and workspace; keys and values
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
