@@ -24,10 +24,10 @@ constexpr int kMaxParts = 64;   // CTAs that may share an item on average
 constexpr int kMinTiles = 4;    // tiles that make a CTA of its own worth while
 constexpr int kJoinSplit = 2;   // CTAs that join an item, each some of its rows
 // Items that can have no more tiles than this are not shared between CTAs (then there is nothing to join), and twice as
-// many where there are items for every CTA.  Measured in a graph (whole, shared) at 8 key heads of dim 128: 64
-// sequences of 500 positions 27 and 33 us, of 1000 39 and 44; one of 500 11 and 9, but its call takes 15.6 and
-// 17.8, which the host's second launch bounds; one of 1000 16 and 9.
-constexpr int kWholeTiles = 16;
+// many where there are items for every other SM.  Measured in a graph (whole, shared) at 8 key heads of dim 128: 64
+// sequences of 500 positions 27 and 33 us; 32, 16, 8 and 4 of 1000 positions 21 and 28, 19 and 21, 18 and 18, 18 and
+// 15; one of 1000 15 and 9.  One of 500 is 11 and 9, but the call takes 13.8 and 17.8, which the host's second launch bounds.
+constexpr int kWholeTiles = 18;
 constexpr int kItemCost = 16;   // what beginning and ending an item takes, in tiles
 // Weights are held as 2^(s - m + kOff), and a score may pass the running maximum m by kLag before
 // that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
@@ -874,8 +874,9 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
     const bool tiles = bf16 && c.dim <= 128 && rows >= kTilesFrom;
     p.rows_max = tiles ? kTilesFrom - 1 : INT32_MAX;
     p.out = out, p.lse = lse, p.status = device_status_ptr();
-    const bool many = (int64_t)bt.batch * c.heads >= 2 * sm_count();
-    p.whole = ((int64_t)bt.max_pages << c.page_log2) <= (many ? 2 : 1) * kWholeTiles * kTile;
+    const bool many = 2 * (int64_t)bt.batch * c.heads >= sm_count();
+    const int64_t span = (int64_t)p.window + 16 / p.group + 2, held = (int64_t)bt.max_pages << c.page_log2;  // as in seq_of()
+    p.whole = (held < span ? held : span) <= (many ? 2 : 1) * kWholeTiles * kTile;
     p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
     if (tiles) {
         const cudaError_t e = launch_kv4_tiles(q, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, ws, s);
