@@ -25,6 +25,15 @@
 // As in kv4_attention.cu, a row's reference moves only when a score passes it by more than kLag,
 // and value steps are divided by a power of two that no step so far is twice as large as; O is
 // rescaled in TMEM in those rare cases alone.
+//
+// What bounds it: a step (both tiles, 128 positions) takes 5700 cycles at dim 128 and 4400 at dim 64, of which
+// the exponentials hold their unit for 2048 and the products the tensor cores for 1700; the rest is the chain
+// product - load - maximum - exponentials - store - product of each tile, which the other tile's covers in part.  S
+// and O fill the tensor memory, so that no third tile fits at dim 128.  Beginning and ending an item takes 6 to 10 us
+// more.  Prompts of 4100, 1999 and 3298 tokens, 32 query heads on 8 of dim 128: 423 us, 614 TFLOP/s.  1024 and 637
+// tokens at the ends of 16500 and 13719 at dim 64: 460 us, 443 TFLOP/s.  Tried, and no faster: S in two halves of 64
+// positions in turns, 16 warps of softmax, exponentials by a polynomial on the fp32 units, weights in columns
+// of their own at dim 64.
 #include "kv4.cuh"
 
 #include <cuda_fp16.h>
@@ -855,7 +864,7 @@ cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts,
     if (T * p.group > INT32_MAX - 2 * kRows || items * 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
     // With few items the positions are split over several CTAs: as many as leave the SMs least idle, where an
     // item costs as much as kCost steps to begin and to end.  (A chunk of 208 items with 130 steps each on 148 SMs: 522 us
-    // unsplit, in two turns of which the second fills two SMs in five; see the table of measurements.)
+    // unsplit, in two turns of which the second fills two SMs in five, and 460 us split.)
     constexpr int kCost = 6;
     const int64_t steps = ceil_div((int64_t)bt.max_pages << c.page_log2, kPos), sms = sm_count();
     int64_t best = -1;
