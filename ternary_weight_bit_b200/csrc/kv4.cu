@@ -15,7 +15,7 @@
 // their way meanwhile).
 //
 // Measured (bf16, dim 128): writing 14,157 rows of 32 key heads (277 MB) takes 84 us, 3.3 TB/s, bound by the
-// issue of instructions (77 % of the slots, 150 to 8 values of a lane); reading 109,000 rows of 8 key heads back (524 MB)
+// issue of instructions (77 % of the slots, 150 to 8 values of a lane); reading 112,186 rows of 8 key heads back (524 MB)
 // takes 99 us, 5.3 TB/s of a copy's 6.5.  Whole rows to a warp's registers in turns, with as many CTAs as fill the
 // SMs once, was slower for reading (144 us, of registers) and no faster for writing.
 #include <type_traits>

@@ -10,7 +10,7 @@
 // padded for groups of up to 8.
 //
 // What bounds it: 64 sequences of 256 to 8192 positions, 32 query heads on 8 of dim 128, one new
-// token each (296 MB of cache): 84 us, 3.5 TB/s; two of 131072 and 111855 positions with 64 query heads:
+// token each (296 MB of cache): 84 us, 3.5 TB/s; two of 131072 and 111869 positions with 64 query heads:
 // 70 us, 3.8 TB/s.  The same kernel without its arithmetic took 75 and 59 us: a tile costs a warp 650 instructions
 // (300 of them turn nibbles into fp16 and 32 are products), which keeps 62 % of the issue slots and half of the
 // integer units busy, and an item's beginning and end take as long as 16 tiles of its CTA.  fp32 calls double
