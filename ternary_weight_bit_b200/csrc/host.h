@@ -140,6 +140,11 @@ cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts,
                              const Kv4Batch &bt, float scale, bool causal, int window, int rows_min, void *out, float *lse,
                              void *ws, cudaStream_t s);
 size_t kv4_tiles_workspace(int64_t T, int group, int heads, int dim, int batch, int rows_min);
+// The same for fp32 calls, and for dim 256 (kv4_chunk.cu).
+cudaError_t launch_kv4_chunks(const void *q, bool bf16, int64_t T, int q_heads, int64_t qts, int64_t qhs, const Kv4Cache &c,
+                              const Kv4Batch &bt, float scale, bool causal, int window, int rows_min, void *out, float *lse,
+                              void *ws, cudaStream_t s);
+size_t kv4_chunk_workspace(int64_t T, int group, int heads, int dim, int batch, int rows_min);
 
 // Argument rules shared by every forward entry point (the workspace is checked by
 // each entry point): BITNET_OK or the status the call returns.

@@ -46,7 +46,7 @@ constexpr float kOff = BF16 ? 3.0f : 13.0f;
 template <bool BF16>
 constexpr float kLag = BF16 ? 11.0f : 1.0f;
 constexpr float kNone = -3.0e38f;  // reference (m - kOff) of a row that has seen nothing yet
-constexpr int kTilesFrom = 128;  // rows of a sequence from which on kv4_prefill.cu takes them
+constexpr int kTilesFrom = 128;  // rows of a sequence from which on kv4_prefill.cu or kv4_chunk.cu takes them
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -867,7 +867,9 @@ size_t kv4_attention_workspace(int64_t T, int q_heads, int heads, int dim, int b
     const int64_t rows = T * (q_heads / heads);
     const size_t tiles = dim <= 128 && rows >= kTilesFrom ? kv4_tiles_workspace(T, q_heads / heads, heads, dim, batch, kTilesFrom) : 0;
     size_t most = one > two ? one : two;
+    const size_t chunk = rows >= kTilesFrom ? kv4_chunk_workspace(T, q_heads / heads, heads, dim, batch, kTilesFrom) : 0;
     most = most > tiles ? most : tiles;
+    most = most > chunk ? most : chunk;
     return (most + 255) & ~(size_t)255;
 }
 
@@ -878,10 +880,10 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
     p.q = q, p.qts = qts, p.qhs = qhs, p.q_heads = q_heads, p.group = q_heads / c.heads, p.T = T;
     p.c = c, p.bt = bt, p.scale = scale, p.causal = causal;
     p.window = window > 0 && window < INT32_MAX ? (int)window : INT32_MAX;
-    // Longer runs of rows go to the tcgen05 kernel where there is one.  max_q is a hint: without that kernel
-    // every sequence is this one's.
+    // Longer runs of rows go to the kernels that unpack a code for 128 rows or more at a time.  max_q is a hint: without
+    // them every sequence is this one's.
     const int64_t rows = (max_q > 0 && max_q < T ? max_q : T) * p.group;
-    const bool tiles = bf16 && c.dim <= 128 && rows >= kTilesFrom;
+    const bool tiles = rows >= kTilesFrom;
     p.rows_max = tiles ? kTilesFrom - 1 : INT32_MAX;
     p.out = out, p.lse = lse, p.status = device_status_ptr();
     const bool many = 2 * (int64_t)bt.batch * c.heads >= sm_count();
@@ -889,7 +891,9 @@ cudaError_t launch_kv4_attention(const void *q, bool bf16, int64_t T, int q_head
     p.whole = (held < span ? held : span) <= (many ? 2 : 1) * kWholeTiles * kTile;
     p.magic[0] = 0x64086408u, p.magic[1] = 0x64806480u;
     if (tiles) {
-        const cudaError_t e = launch_kv4_tiles(q, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, ws, s);
+        const cudaError_t e = bf16 && c.dim <= 128
+                                  ? launch_kv4_tiles(q, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, ws, s)
+                                  : launch_kv4_chunks(q, bf16, T, q_heads, qts, qhs, c, bt, scale, causal, p.window, kTilesFrom, out, lse, ws, s);
         if (e != cudaSuccess) return e;
     }
     const bool two = rows > 8;
