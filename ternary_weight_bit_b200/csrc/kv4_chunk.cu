@@ -16,7 +16,8 @@
 // What bounds it: a prompt of 2048 tokens, 32 query heads on 8, takes 228 us in fp32 at dim 128 (two products to
 // each of the formula's: 301 TFLOP/s of them) and 297 in bf16 at dim 256 (231 TFLOP/s), against 550 and 943 of
 // kv4_rows_kernel.  The tensor cores' mma.sync path is busy for 54 and 42 % of the time; unpacking
-// and the two barriers of a step are not covered by products, as one CTA fills an SM's registers.
+// and the two barriers of a step are not covered by products, as one CTA fills an SM's registers.  Tried, and no
+// faster: two steps' tiles with one barrier a step (232 and 314), products in groups of four sums.
 #include "kv4.cuh"
 
 #include <cuda_fp16.h>
