@@ -378,6 +378,27 @@ def test_a_query_that_is_not_finite_keeps_to_its_row(new):
         assert torch.equal(out[keep], good[keep])
 
 
+@pytest.mark.parametrize("new", [1, 30, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("pos", [0, 5, 250])
+def test_a_step_that_is_not_finite_keeps_to_the_rows_that_see_it(pos, dtype, new):
+    batch = Batch([300], [new], 64)
+    c, _ = filled(batch, 2, 128, 64)
+    q = queries(new, 4, 128, dtype)
+    for window in (0, 60):
+        want, _ = run_attention(batch, c, q, window=window)
+        for side, bad in (("v_step", math.inf), ("v_step", math.nan), ("k_step", math.nan)):
+            step = getattr(c, side)[int(batch.table[0, pos // 64]), 1]
+            kept = step[pos % 64].clone()
+            step[pos % 64] = bad
+            got, _ = run_attention(batch, c, q, window=window)
+            step[pos % 64] = kept
+            at = torch.arange(300 - new, 300)
+            sees = (at >= pos) & ((at - pos < window) | (window == 0))
+            assert got[sees.to(DEV), 2:].isnan().all()
+            assert torch.equal(got[:, :2], want[:, :2]) and torch.equal(got[~sees.to(DEV)], want[~sees.to(DEV)])
+
+
 @pytest.mark.parametrize("new", [1, 50, 200])
 def test_attention_takes_strided_queries_and_gives_equal_bits(new):
     batch = Batch([333, 90], [new, 3], 16)
