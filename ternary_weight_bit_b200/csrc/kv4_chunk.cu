@@ -35,6 +35,7 @@ constexpr float kOff = BF16 ? 3.0f : 13.0f;
 template <bool BF16>
 constexpr float kLag = BF16 ? 11.0f : 1.0f;
 constexpr float kNone = -3.0e38f;
+constexpr int kSplits = 8;  // parts of an item at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct ChunkParams {
@@ -492,7 +493,6 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
     constexpr int64_t kPart = (D + 2) * kRows;
     __shared__ float out[32][D + 1];
-    __shared__ float sums[32];
     __shared__ int64_t places[32];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
@@ -502,24 +502,42 @@ __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_consta
     if (place >= p.T * p.q_heads) place = -1;  // a workspace that calls share at the same time can hold anything
     if (__syncthreads_and(place < 0)) return;  // nobody's rows, whose parts may not be written
     const float *const src = p.part + (int64_t)item * p.splits * kPart + row;
-    float top = kNone, sum = 0.0f;
-    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, src[s * kPart + D * kRows]);
-    for (int s = 0; s < p.splits; ++s) sum = fmaf(ex2(src[s * kPart + D * kRows] - top), src[s * kPart + (D + 1) * kRows], sum);
+    // everything of a row at a time: the references and sums, then eight parts of four dimensions
+    float w[kSplits], l[kSplits], top = kNone, sum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kSplits; ++s) {
+        w[s] = s < p.splits ? src[s * kPart + D * kRows] : kNone;
+        l[s] = s < p.splits ? src[s * kPart + (D + 1) * kRows] : 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < kSplits; ++s) top = fmaxf(top, w[s]);
+#pragma unroll
+    for (int s = 0; s < kSplits; ++s) w[s] = ex2(w[s] - top), sum = fmaf(w[s], l[s], sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (warp == 0) {
         places[lane] = place;
-        sums[lane] = sum == 0.0f ? 0.0f : 1.0f / sum;
         if (p.lse && place >= 0) p.lse[place] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
     }
-    for (int d = warp; d < D; d += 8) {
-        float y = 0.0f;
-        for (int s = 0; s < p.splits; ++s) y = fmaf(ex2(src[s * kPart + D * kRows] - top), src[s * kPart + d * kRows], y);
-        out[lane][d] = y;
+#pragma unroll
+    for (int d0 = 0; d0 < D / 8; d0 += 4) {
+        float v[4][kSplits];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int s = 0; s < kSplits; ++s) v[e][s] = s < p.splits ? src[s * kPart + (8 * (d0 + e) + warp) * kRows] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float y = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSplits; ++s) y = fmaf(w[s], v[e][s], y);
+            out[lane][8 * (d0 + e) + warp] = y * inv;
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * D; i += 256) {
         const int r = i / D, d = i % D;
         if (places[r] < 0) continue;
-        const float y = out[r][d] * sums[r];
+        const float y = out[r][d];
         if constexpr (BF16) static_cast<__nv_bfloat16 *>(p.out)[places[r] * D + d] = __float2bfloat16_rn(y);
         else static_cast<float *>(p.out)[places[r] * D + d] = y;
     }
@@ -563,7 +581,7 @@ int64_t most_items(int64_t T, int group, int heads, int batch, int rows_min) {
 // Parts of split items: up to three of them to an SM.
 int64_t most_splits(int64_t items) {
     const int64_t s = items > 0 ? (int64_t)3 * sm_count() / items : 0;
-    return s < 1 ? 1 : (s > 8 ? 8 : s);
+    return s < 1 ? 1 : (s > kSplits ? kSplits : s);
 }
 
 }  // namespace
@@ -587,12 +605,12 @@ cudaError_t launch_kv4_chunks(const void *q, bool bf16, int64_t T, int q_heads, 
     if (T * p.group > INT32_MAX - kRows || items * 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
     // With few items the positions are split over several CTAs, as many as leave the SMs least idle; an item costs
     // as much as kCost steps to begin and to end.
-    constexpr int kCost = 4;
+    constexpr int kCost = 4, kJoin = 2;
     const int64_t steps = ceil_div((int64_t)bt.max_pages << c.page_log2, kPos), sms = sm_count();
     int64_t best = -1;
     p.splits = 1;
-    for (int64_t n = 1; n <= most_splits(items) && (n == 1 || steps >= 8 * n); ++n) {
-        const int64_t cost = ceil_div(items * n, sms) * (kCost + ceil_div(steps, n) + (n > 1 ? 1 : 0));
+    for (int64_t n = 1; n <= most_splits(items) && (n == 1 || steps >= 2 * n); ++n) {
+        const int64_t cost = ceil_div(items * n, sms) * (kCost + ceil_div(steps, n)) + (n > 1 ? kJoin : 0);
         if (best < 0 || cost < best) best = cost, p.splits = (int)n;
     }
     p.place = static_cast<int64_t *>(ws);

@@ -57,6 +57,7 @@ template <int D>
 constexpr int kOtherRegs = 256 - kSoftmaxRegs<D>;
 constexpr uint32_t kNowhere = 0xffffffffu;
 constexpr float kOff = 3.0f, kLag = 11.0f, kNone = -3.0e38f;
+constexpr int kSplits = 8;  // parts of an item at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // n / d for 0 <= n < 2^31 by a multiplication: with 2^l >= d, m = floor(2^32 (2^l - d) / d) + 1.
@@ -762,7 +763,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
 template <int D>
 __global__ void __launch_bounds__(256) kv4_tiles_join_kernel(const __grid_constant__ TileParams p) {
     __shared__ float out[32][D + 1];
-    __shared__ float sums[32];
     __shared__ int64_t places[32];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
@@ -773,26 +773,42 @@ __global__ void __launch_bounds__(256) kv4_tiles_join_kernel(const __grid_consta
     int64_t place = p.place[(int64_t)item * (2 * kRows) + row];
     if (place >= p.T * p.q_heads) place = -1;  // a workspace that calls share at the same time can hold anything
     if (__syncthreads_and(place < 0)) return;  // nobody's rows, whose parts may not be written
-    float top = kNone, sum = 0.0f;
-    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, src[s * kPart + D * (2 * kRows)]);
-    for (int s = 0; s < p.splits; ++s)
-        sum = fmaf(ex2(src[s * kPart + D * (2 * kRows)] - top), src[s * kPart + (D + 1) * (2 * kRows)], sum);
+    // everything of a row at a time: the references and sums, then eight parts of four dimensions
+    float w[kSplits], l[kSplits], top = kNone, sum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kSplits; ++s) {
+        w[s] = s < p.splits ? src[s * kPart + D * (2 * kRows)] : kNone;
+        l[s] = s < p.splits ? src[s * kPart + (D + 1) * (2 * kRows)] : 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < kSplits; ++s) top = fmaxf(top, w[s]);
+#pragma unroll
+    for (int s = 0; s < kSplits; ++s) w[s] = ex2(w[s] - top), sum = fmaf(w[s], l[s], sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (warp == 0) {
         places[lane] = place;
-        sums[lane] = sum == 0.0f ? 0.0f : 1.0f / sum;
         if (p.lse && place >= 0) p.lse[place] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
     }
-    for (int d = warp; d < D; d += 8) {
-        float y = 0.0f;
-        for (int s = 0; s < p.splits; ++s)
-            y = fmaf(ex2(src[s * kPart + D * (2 * kRows)] - top), src[s * kPart + d * (2 * kRows)], y);
-        out[lane][d] = y;
+#pragma unroll
+    for (int d0 = 0; d0 < D / 8; d0 += 4) {
+        float v[4][kSplits];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int s = 0; s < kSplits; ++s) v[e][s] = s < p.splits ? src[s * kPart + (8 * (d0 + e) + warp) * (2 * kRows)] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float y = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSplits; ++s) y = fmaf(w[s], v[e][s], y);
+            out[lane][8 * (d0 + e) + warp] = y * inv;
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * (D / 2); i += 256) {
         const int r = i / (D / 2), d = 2 * (i % (D / 2));
         if (places[r] >= 0)
-            *reinterpret_cast<uint32_t *>(p.out + places[r] * D + d) = bf2(out[r][d] * sums[r], out[r][d + 1] * sums[r]);
+            *reinterpret_cast<uint32_t *>(p.out + places[r] * D + d) = bf2(out[r][d], out[r][d + 1]);
     }
 }
 
@@ -839,7 +855,7 @@ int64_t most_items(int64_t T, int group, int heads, int batch, int rows_min) {
 constexpr int kWaves = 3;
 int64_t most_splits(int64_t items) {
     const int64_t s = items > 0 ? (int64_t)kWaves * sm_count() / items : 0;
-    return s < 1 ? 1 : (s > 8 ? 8 : s);
+    return s < 1 ? 1 : (s > kSplits ? kSplits : s);
 }
 
 }  // namespace
