@@ -31,7 +31,7 @@
 // product - load - maximum - exponentials - store - product of each tile, which the other tile's covers in part.  S
 // and O fill the tensor memory, so that no third tile fits at dim 128.  Beginning and ending an item takes 6 to 10 us
 // more.  Prompts of 4100, 1999 and 3298 tokens, 32 query heads on 8 of dim 128: 423 us, 614 TFLOP/s.  1024 and 637
-// tokens at the ends of 16500 and 13719 at dim 64: 460 us, 443 TFLOP/s.  Tried, and no faster: S in two halves of 64
+// tokens at the ends of 16500 and 13719 at dim 64: 456 us, 447 TFLOP/s.  Tried, and no faster: S in two halves of 64
 // positions in turns, 16 warps of softmax, exponentials by a polynomial on the fp32 units, weights in columns
 // of their own at dim 64.
 #include "kv4.cuh"
@@ -880,13 +880,14 @@ cudaError_t launch_kv4_tiles(const void *q, int64_t T, int q_heads, int64_t qts,
     if (T * p.group > INT32_MAX - 2 * kRows || items * 8 > INT32_MAX) return cudaErrorInvalidConfiguration;
     // With few items the positions are split over several CTAs: as many as leave the SMs least idle, where an
     // item costs as much as kCost steps to begin and to end.  (A chunk of 208 items with 130 steps each on 148 SMs: 522 us
-    // unsplit, in two turns of which the second fills two SMs in five, and 460 us split.)
-    constexpr int kCost = 6;
+    // unsplit, in two turns of which the second fills two SMs in five, and 456 us split; 700 tokens of one head of dim 128:
+    // 31 and 28.)  Joining costs about a step.
+    constexpr int kCost = 6, kJoin = 1;
     const int64_t steps = ceil_div((int64_t)bt.max_pages << c.page_log2, kPos), sms = sm_count();
     int64_t best = -1;
     p.splits = 1;
-    for (int64_t n = 1; n <= most_splits(items) && (n == 1 || steps >= 8 * n); ++n) {
-        const int64_t cost = ceil_div(items * n, sms) * (kCost + ceil_div(steps, n) + (n > 1 ? 1 : 0));
+    for (int64_t n = 1; n <= most_splits(items) && (n == 1 || steps >= 2 * n); ++n) {
+        const int64_t cost = ceil_div(items * n, sms) * (kCost + ceil_div(steps, n)) + (n > 1 ? kJoin : 0);
         if (best < 0 || cost < best) best = cost, p.splits = (int)n;
     }
     p.place = static_cast<int64_t *>(ws);
