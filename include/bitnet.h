@@ -398,7 +398,8 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *   q_heads  a multiple of heads, at most 32768, with T * q_heads < 2^31
  *            (BITNET_ERR_UNSUPPORTED_SHAPE).  window >= 0, and 0 unless causal.
  *   max_q    0, or the largest n_b of the batch where the caller knows it (a hint for
- *            the choice of kernel; results stay right where it is wrong).
+ *            the choice of kernel; results stay right where it is wrong).  Worth giving where
+ *            T counts many rows that belong to no sequence.
  *   ws       device scratch of at least bitnet_kv4_attention_workspace_bytes(...) bytes
  *            (256-byte aligned; BITNET_ERR_WORKSPACE if smaller).  Its contents need no
  *            initialisation.  Calls that may run at the same time need one each.

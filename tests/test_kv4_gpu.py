@@ -378,6 +378,17 @@ def test_a_query_that_is_not_finite_keeps_to_its_row(new):
         assert torch.equal(out[keep], good[keep])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [0, 1, 3, 70])
+def test_one_sequence_with_few_of_many_rows(new, dim, dtype):
+    batch = Batch([max(new, 300)], [new], 32, lead=30, tail=200)
+    c, held = filled(batch, 2, dim, 32)
+    q = queries(batch.rows, 8, dim, dtype)
+    out, lse = run_attention(batch, c, q)
+    check_attention(batch, c, held, q, out, lse, dim ** -0.5, True, 0)
+
+
 @pytest.mark.parametrize("new", [1, 30, 200])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("pos", [0, 5, 250])
