@@ -575,7 +575,8 @@ def bitnet_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Te
     """Softmax attention of q [T, q_heads, dim] (fp32 or bf16, any token and head strides) over the cached keys and
     values of each row's sequence; query head h reads key head h // (q_heads // heads).  scale defaults to
     dim ** -0.5; window > 0 limits a causal row to its last `window` positions; max_q, the largest number
-    of rows of a sequence, is a hint for the choice of kernel (worth giving where q has many rows of nobody).  Rows that see nothing give zeros (lse -inf).
+    of rows of a sequence, is a hint for the choice of kernel (worth giving where q has many rows of nobody).
+    Rows that see nothing give zeros (lse -inf).
 
     Returns out [T, q_heads, dim] of q's dtype, or (out, lse fp32 [T, q_heads]) with return_lse.  Calls that may
     run at the same time need workspaces of their own."""

@@ -79,18 +79,26 @@ __device__ __forceinline__ void locate_tokens(const Kv4Cache &c, const Kv4Batch 
 
 // A lane's rows: those of one token and side, heads first, first + step, ...  The token goes
 // fastest over the warps' rows, so that neighbouring rows of the cache are moved together.
-template <int D, int ITER>
+// Where the heads are too FEW to fill a CTA so, it takes one head of kSet * ITER tokens: tok, tok + kSet, ...
+template <int D, int ITER, bool FEW>
 struct Rows {
+    static constexpr int kTokens = FEW ? kSet<D> * ITER : kMaxTokens<D>;
     int tok, first, step;
     bool side;  // values
     __device__ __forceinline__ Rows(int tokens_log2) {
         const int warp = threadIdx.x >> 5;
-        const int r = blockIdx.y * (kSet<D> * ITER) + (warp & (kWarps / 2 - 1)) * (256 / D) + (threadIdx.x & 31) / (D / 8);
-        tok = r & ((1 << tokens_log2) - 1);
-        first = r >> tokens_log2;
-        step = kSet<D> >> tokens_log2;
+        const int r = (warp & (kWarps / 2 - 1)) * (256 / D) + (threadIdx.x & 31) / (D / 8);
+        if constexpr (FEW) {
+            tok = r, first = blockIdx.y, step = 0;
+        } else {
+            const int of = blockIdx.y * (kSet<D> * ITER) + r;
+            tok = of & ((1 << tokens_log2) - 1);
+            first = of >> tokens_log2;
+            step = kSet<D> >> tokens_log2;
+        }
         side = __shfl_sync(0xffffffffu, warp, 0) >= kWarps / 2;
     }
+    __device__ __forceinline__ int token(int it) const { return FEW ? tok + it * kSet<D> : tok; }
 };
 
 // A NaN in a row makes its step NaN, so that it is not lost.
@@ -113,23 +121,25 @@ constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves rne(t) in
 // adds in a lane, 5 in the tree, the scale's addition, the reciprocal at two, the constant and
 // its product), 17 * 2^-24 zero, and the roundings of u and zero / n, n 2^-24: together below
 // 1.15e-6 zero.  So where n u is further than 1.25e-6 zero from a half-integer, its level is the
-// exact value's.  About 1 row in 200 of 4-bit rows has a value nearer than that; its warp, and
+// exact value's.  (3 bits: a maximum has no roundings, which leaves 5, 0.42e-6 zero in all; halves of the
+// maximum, frequent in bf16, are only 1.5 eps / max from a border.)  About 1 row in 200 of 4-bit rows has a value nearer than that; its warp, and
 // that of a position 0, forms the statistic and the products again in fp64.
-template <bool BF16, int D, int BITS>
+template <bool BF16, int D, int BITS, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps, BF16 ? 4 : 3)
 kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t T, int64_t kts, int64_t khs,
                  int64_t vts, int64_t vhs, Kv4Cache c, Kv4Batch bt, float eps, int tokens_log2, int *status) {
     constexpr int LPR = D / 8, kIter = kWriteIter;
     static_assert(kIter <= LPR, "lane i of a row keeps the step of iteration i");
     constexpr double kQ = BITS == 4 ? 2.6457513110645905905 : 3.0;
-    constexpr float kZero = BITS == 4 ? 8.0f : 4.0f, kLevels = 2.0f * kZero - 1.0f;
-    __shared__ Place place[kMaxTokens<D>];
+    constexpr float kZero = BITS == 4 ? 8.0f : 4.0f, kLevels = 2.0f * kZero - 1.0f, kNear = BITS == 4 ? 1.25e-6f : 0.45e-6f;
+    using R = Rows<D, kIter, FEW>;
+    __shared__ Place place[R::kTokens];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int lane = threadIdx.x & 31;
     const int p = lane % LPR;
-    const int t0 = blockIdx.x << tokens_log2;
-    const Rows<D, kIter> id(tokens_log2);
+    const int t0 = FEW ? blockIdx.x * R::kTokens : blockIdx.x << tokens_log2;
+    const R id(tokens_log2);
     const int heads = c.heads;
     int live = 0;  // the lane's heads; lane 0 has the warp's most
 #pragma unroll
@@ -138,24 +148,31 @@ kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t
     Raw<BF16> raw[kIter];
     {
         constexpr int kSize = BF16 ? 2 : 4;
-        const int count = t0 + id.tok < T ? live : 0;
-        const int64_t hs = id.side ? vhs : khs;
-        const char *from = static_cast<const char *>(id.side ? v : k) + ((t0 + id.tok) * (id.side ? vts : kts) + id.first * hs + 8 * p) * kSize;
-        const int64_t stride = id.step * hs * kSize;
+        const int64_t ts = id.side ? vts : kts, hs = id.side ? vhs : khs;
+        const int count = FEW ? (int)min((int64_t)kIter, (T - t0 - id.tok + kSet<D> - 1) / kSet<D>) : (t0 + id.tok < T ? live : 0);
+        const char *from = static_cast<const char *>(id.side ? v : k) + ((t0 + id.tok) * ts + id.first * hs + 8 * p) * kSize;
+        const int64_t stride = (FEW ? kSet<D> * ts : id.step * hs) * kSize;
 #pragma unroll
         for (int it = 0; it < kIter; ++it, from += stride) raw[it].load(from, it < count);
     }
-    locate_tokens(c, bt, t0, 1 << tokens_log2, T, status, place);
-    const Place at = place[id.tok];
-    const int64_t first = kv4_rows(c, max(at.page, 0), id.first) + at.row, stride = (int64_t)id.step << c.page_log2;
-    uint8_t *codes = (id.side ? c.v_codes : c.k_codes) + first * (D / 2) + 4 * p;
-    const int count = at.page >= 0 ? live : 0;
-    const bool bos = at.pos == 0;
+    locate_tokens(c, bt, t0, FEW ? R::kTokens : 1 << tokens_log2, T, status, place);
+    Place at = place[id.tok];
+    int64_t first = kv4_rows(c, max(at.page, 0), id.first) + at.row;
+    const int64_t stride = (int64_t)id.step << c.page_log2;
+    uint8_t *const all_codes = id.side ? c.v_codes : c.k_codes;
+    uint8_t *codes = all_codes + first * (D / 2) + 4 * p;
     float own = 0.0f;  // of iteration p: the scale, or the step where fp64 gave it
     bool is_step = false;
 #pragma unroll
     for (int it = 0; it < kIter; ++it, codes += stride * (D / 2)) {
         if (it >= most_live) break;
+        if (FEW && it > 0) {
+            at = place[id.token(it)];
+            first = kv4_rows(c, max(at.page, 0), id.first) + at.row;
+            codes = all_codes + first * (D / 2) + 4 * p;
+        }
+        const int count = at.page >= 0 ? live : 0;
+        const bool bos = at.pos == 0;
         float x[8], a = 0.0f;
         raw[it].values(x);
 #pragma unroll
@@ -179,27 +196,31 @@ kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t
         const float hi = fmaf(fmaf(fmaf(f[7] + 2048.0f, 16.0f, f[6]), 16.0f, f[5]), 16.0f, f[4]);
         uint32_t w = (__byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410) + (BITS == 4 ? 0u : 0x44444444u)) ^ 0x88888888u;
         if (p == it) own = scale;
-        const uint32_t asks = __ballot_sync(0xffffffffu, bos || !(scale >= 1e-36f && scale <= 1e36f && most < 0.5f - 1.25e-6f * kZero));
+        const uint32_t asks = __ballot_sync(0xffffffffu, bos || !(scale >= 1e-36f && scale <= 1e36f && most < 0.5f - kNear * kZero));
         if (asks) {
             // the rows of a warp may differ in kind; every lane takes the same shuffles, and only
             // the rows that ask for it change, so that a row's step does not depend on its neighbours
             const bool mean = BITS == 4 && !bos;
-            double sum = 0.0;
+            double sum = a;  // 3 bits: the maximum, exact already
+            float nan = a;
+            if constexpr (BITS == 4) {
+                sum = 0.0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double m = fabs((double)x[e]);
-                sum = mean ? sum + m : fmax(sum, m);
+                for (int e = 0; e < 8; ++e) {
+                    const double m = fabs((double)x[e]);
+                    sum = mean ? sum + m : fmax(sum, m);
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) {
+                    const double b = __shfl_xor_sync(0xffffffffu, sum, o);
+                    sum = mean ? sum + b : fmax(sum, b);
+                }
+                nan = fabsf(x[0]);
+#pragma unroll
+                for (int e = 1; e < 8; ++e) nan = max_nan(nan, fabsf(x[e]));
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) nan = max_nan(nan, __shfl_xor_sync(0xffffffffu, nan, o));
             }
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) {
-                const double b = __shfl_xor_sync(0xffffffffu, sum, o);
-                sum = mean ? sum + b : fmax(sum, b);
-            }
-            float nan = fabsf(x[0]);
-#pragma unroll
-            for (int e = 1; e < 8; ++e) nan = max_nan(nan, fabsf(x[e]));
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) nan = max_nan(nan, __shfl_xor_sync(0xffffffffu, nan, o));
             if (asks >> (lane & ~(LPR - 1)) & (0xffffffffu >> (32 - LPR))) {
                 const double q = bos ? 127.0 : kQ, zero = bos ? 128.0 : (double)kZero;
                 const double sd = (mean ? sum / D : sum) + (double)eps;
@@ -220,7 +241,11 @@ kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t
         }
         if (it < count) *reinterpret_cast<uint32_t *>(codes) = w;
     }
-    if (p < count)
+    if (FEW && p < kIter) {
+        at = place[id.token(p)];
+        first = kv4_rows(c, max(at.page, 0), id.first) + at.row;
+    }
+    if (p < live && at.page >= 0)
         (id.side ? c.v_step : c.k_step)[first + p * stride] = is_step ? own : __fdiv_rn(own, (float)kQ);
 }
 
@@ -228,34 +253,40 @@ kv4_write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t
 // 2^(23 - 4 e), is that plus the nibble exactly; less 2^(23 - 4 e) + 8 it is the code.
 // Lane p of a row writes values 8 p .. 8 p + 7 of it (bf16), or 4 p .. and 4 (p + D / 8) .. (fp32),
 // so that a store's lanes lie side by side.
-template <bool BF16, int D>
+template <bool BF16, int D, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps)
 kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, void *__restrict__ v_out,
                 int tokens_log2, int *status) {
     constexpr int LPR = D / 8, kIter = kReadIter;
-    __shared__ Place place[kMaxTokens<D>];
+    using R = Rows<D, kIter, FEW>;
+    __shared__ Place place[R::kTokens];
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int p = (threadIdx.x & 31) % LPR;
-    const int t0 = blockIdx.x << tokens_log2;
-    const Rows<D, kIter> id(tokens_log2);
+    const int t0 = FEW ? blockIdx.x * R::kTokens : blockIdx.x << tokens_log2;
+    const R id(tokens_log2);
     const int heads = c.heads;
-    locate_tokens(c, bt, t0, 1 << tokens_log2, T, status, place);
-    const Place at = place[id.tok];
+    locate_tokens(c, bt, t0, FEW ? R::kTokens : 1 << tokens_log2, T, status, place);
+    Place at = place[id.tok];
     void *const out = id.side ? v_out : k_out;
-    if (at.pos == INT32_MIN || !out) return;
-    const bool on = at.page >= 0, bos = at.pos == 0;
-    const int64_t first = kv4_rows(c, max(at.page, 0), id.first) + at.row, stride = (int64_t)id.step << c.page_log2;
-    const uint8_t *const codes = (id.side ? c.v_codes : c.k_codes) + first * (D / 2);
-    const float *const steps = (id.side ? c.v_step : c.k_step) + first;
+    if ((!FEW && at.pos == INT32_MIN) || !out) return;
+    int64_t first = kv4_rows(c, max(at.page, 0), id.first) + at.row;
+    const int64_t stride = (int64_t)id.step << c.page_log2;
+    const uint8_t *const codes = id.side ? c.v_codes : c.k_codes;
+    const float *const steps = id.side ? c.v_step : c.k_step;
     uint32_t w[kIter];
     float step[kIter];
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
         w[it] = 0x88888888u, step[it] = 0.0f;
-        if (on && id.first + it * id.step < heads) {
-            const uint8_t *const from = codes + it * stride * (D / 2);
-            step[it] = steps[it * stride];
+        if (FEW && it > 0) {
+            at = place[id.token(it)];
+            first = kv4_rows(c, max(at.page, 0), id.first) + at.row;
+        }
+        if (at.page >= 0 && id.first + it * id.step < heads) {
+            const int64_t row = FEW ? first : first + it * stride;
+            const uint8_t *const from = codes + row * (D / 2);
+            step[it] = steps[row];
             if constexpr (BF16) {
                 w[it] = *reinterpret_cast<const uint32_t *>(from + 4 * p);
             } else {
@@ -269,6 +300,12 @@ kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, vo
     for (int it = 0; it < kIter; ++it) {
         const int head = id.first + it * id.step;
         if (head >= heads) break;
+        if (FEW) {
+            at = place[id.token(it)];
+            if (at.pos == INT32_MIN) continue;
+        }
+        const bool on = at.page >= 0, bos = at.pos == 0;
+        const int64_t to = o + (FEW ? (int64_t)it * kSet<D> * heads * D : it * id.step * D);
         float y[8];
         if (bos) {
             const int8_t *const c8 = (id.side ? c.v_bos : c.k_bos) + ((int64_t)max(at.page, 0) * heads + head) * D;
@@ -290,9 +327,9 @@ kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, vo
                 const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
                 h[e] = *reinterpret_cast<const uint32_t *>(&b);
             }
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + o + it * id.step * D) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + to) = make_uint4(h[0], h[1], h[2], h[3]);
         } else {
-            float *const d = reinterpret_cast<float *>(out) + o + it * id.step * D;
+            float *const d = reinterpret_cast<float *>(out) + to;
             *reinterpret_cast<float4 *>(d) = make_float4(y[0], y[1], y[2], y[3]);
             *reinterpret_cast<float4 *>(d + D / 2) = make_float4(y[4], y[5], y[6], y[7]);
         }
@@ -302,18 +339,22 @@ kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, vo
 struct RowGrid {
     dim3 grid;
     int tokens_log2;
+    bool few;
 };
 // Tokens of a CTA: as many as fill a CTA, and at least eight (neighbouring rows of the cache
-// are then moved together), as long as that leaves eight CTAs to an SM.
+// are then moved together), as long as that leaves eight CTAs to an SM.  Few heads that do not
+// fill a CTA so have CTAs of their own, with more tokens (one head of 524,288 rows of dim 128 in bf16 is read at 5000 GB/s
+// instead of 1900 and written at 3300 instead of 1650).
 RowGrid row_grid(int64_t T, int heads, int D, int iter) {
-    RowGrid g;
-    const int set = kWarps / 2 * (256 / D), per_cta = set * iter;
+    const int set = kWarps / 2 * (256 / D), per_cta = set * iter, most = set < 16 ? set : 16;
+    auto fills = [](dim3 g) { return (int64_t)g.x * g.y >= 8 * (int64_t)sm_count(); };
+    const dim3 few((unsigned)ceil_div(T, per_cta), (unsigned)heads);
+    if (heads * most < per_cta && fills(few)) return {few, 0, true};
     auto grid = [&](int log2) { return dim3((unsigned)ceil_div(T, 1 << log2), (unsigned)ceil_div((int64_t)heads << log2, per_cta)); };
-    g.tokens_log2 = 0;
-    for (int log2 = 1; (1 << log2) <= (set < 16 ? set : 16) && (log2 <= 3 || heads << log2 <= per_cta); ++log2)
-        if ((int64_t)grid(log2).x * grid(log2).y >= 8 * (int64_t)sm_count()) g.tokens_log2 = log2;
-    g.grid = grid(g.tokens_log2);
-    return g;
+    int tokens_log2 = 0;
+    for (int log2 = 1; (1 << log2) <= most && (log2 <= 3 || heads << log2 <= per_cta); ++log2)
+        if (fills(grid(log2))) tokens_log2 = log2;
+    return {grid(tokens_log2), tokens_log2, false};
 }
 
 template <typename... P, typename... A>
@@ -337,16 +378,17 @@ cudaError_t launch_kv4_write(const void *k, const void *v, bool bf16, int64_t T,
     const RowGrid g = row_grid(T, c.heads, c.dim, kWriteIter);
     int *status = device_status_ptr();
     auto go = [&](auto kernel) { return launch_rows(kernel, g.grid, s, k, v, T, kts, khs, vts, vhs, c, bt, eps, g.tokens_log2, status); };
-    auto of = [&](auto type, auto n) {
-        constexpr bool kBf16 = decltype(type)::value;
+    auto of = [&](auto type, auto n, auto few) {
+        constexpr bool kBf16 = decltype(type)::value, kFew = decltype(few)::value;
         constexpr int kBits = decltype(n)::value;
-        if (c.dim == 64) return go(kv4_write_kernel<kBf16, 64, kBits>);
-        if (c.dim == 128) return go(kv4_write_kernel<kBf16, 128, kBits>);
-        return go(kv4_write_kernel<kBf16, 256, kBits>);
+        if (c.dim == 64) return go(kv4_write_kernel<kBf16, 64, kBits, kFew>);
+        if (c.dim == 128) return go(kv4_write_kernel<kBf16, 128, kBits, kFew>);
+        return go(kv4_write_kernel<kBf16, 256, kBits, kFew>);
     };
+    auto with = [&](auto type, auto n) { return g.few ? of(type, n, std::true_type()) : of(type, n, std::false_type()); };
     using std::integral_constant;
-    if (bits == 4) return bf16 ? of(std::true_type(), integral_constant<int, 4>()) : of(std::false_type(), integral_constant<int, 4>());
-    return bf16 ? of(std::true_type(), integral_constant<int, 3>()) : of(std::false_type(), integral_constant<int, 3>());
+    if (bits == 4) return bf16 ? with(std::true_type(), integral_constant<int, 4>()) : with(std::false_type(), integral_constant<int, 4>());
+    return bf16 ? with(std::true_type(), integral_constant<int, 3>()) : with(std::false_type(), integral_constant<int, 3>());
 }
 
 cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &bt, int64_t T, void *k_out, void *v_out, bool bf16,
@@ -356,9 +398,14 @@ cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &bt, int64_t T, vo
     auto go = [&](auto kernel) {
         return launch_rows(kernel, g.grid, s, c, bt, T, k_out, v_out, g.tokens_log2, status);
     };
-    if (c.dim == 64) return bf16 ? go(kv4_read_kernel<true, 64>) : go(kv4_read_kernel<false, 64>);
-    if (c.dim == 128) return bf16 ? go(kv4_read_kernel<true, 128>) : go(kv4_read_kernel<false, 128>);
-    return bf16 ? go(kv4_read_kernel<true, 256>) : go(kv4_read_kernel<false, 256>);
+    auto of = [&](auto type, auto few) {
+        constexpr bool kBf16 = decltype(type)::value, kFew = decltype(few)::value;
+        if (c.dim == 64) return go(kv4_read_kernel<kBf16, 64, kFew>);
+        if (c.dim == 128) return go(kv4_read_kernel<kBf16, 128, kFew>);
+        return go(kv4_read_kernel<kBf16, 256, kFew>);
+    };
+    auto with = [&](auto type) { return g.few ? of(type, std::true_type()) : of(type, std::false_type()); };
+    return bf16 ? with(std::true_type()) : with(std::false_type());
 }
 
 }  // namespace bitnet

@@ -149,6 +149,30 @@ def test_write_of_many_rows_has_the_exact_codes():
         assert torch.equal(y[place[:, 0]], step[..., None] * want.float())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("heads,dim,page,bits", [(1, 64, 16, 4), (1, 128, 64, 3), (3, 128, 16, 4), (2, 256, 64, 4), (3, 64, 256, 3), (1, 256, 32, 3)])
+def test_many_rows_of_few_heads_are_those_of_more_heads(heads, dim, page, bits, dtype):
+    """Many rows of few heads take another path of the kernels than the same rows among 16 heads."""
+    batch = Batch([30000, 29000, 3000], [30000, 27001, 2500], page, lead=5, tail=9)
+    k, v = (rows_like_keys((batch.rows, 16, dim), s).to(DTYPES[dtype]).to(DEV) for s in (1, 2))
+    few, more = (rubbish_cache(batch.pages, h, dim, page) for h in (heads, 16))
+    tensors = batch.tensors(DEV)
+    for n in ("k_codes", "v_codes", "k_bos", "v_bos"):
+        getattr(few, n).copy_(getattr(more, n)[:, :heads])  # the same rubbish
+    tb.bitnet_kv4_write(k[:, :heads], v[:, :heads], few, *tensors, bits=bits)
+    tb.bitnet_kv4_write(k, v, more, *tensors, bits=bits)
+    for n, t in copies(few).items():
+        same = getattr(more, n)[:, :heads].cpu()
+        assert torch.equal(torch.nan_to_num(t.float(), 7e37, 8e37), torch.nan_to_num(same.float(), 7e37, 8e37)), n
+    outs = []
+    for c, h in ((few, heads), (more, 16)):
+        out = [torch.full((batch.rows, h, dim), 123.0, dtype=DTYPES[dtype], device=DEV) for _ in range(2)]
+        tb.bitnet_kv4_read(c, *tensors, batch.rows, dtype=DTYPES[dtype], k_out=out[0], v_out=out[1])
+        outs.append(out)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b[:, :heads]) and (a[:5] == 123.0).all() and (a[-9:] == 123.0).all()
+
+
 @pytest.mark.parametrize("scale", [1e-38, 1e-20, 1e18, 2e36])
 def test_write_of_tiny_and_huge_rows(scale):
     x = rows_like_keys((20, 2, 128), 5) * scale
