@@ -529,6 +529,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             fetch(it + kStages<D, NT, BF16> - 1, slot_in);
             advance(slot_in);
             copies_wait<kStages<D, NT, BF16> - 1>();
+            __syncwarp();  // a lane waits for its own copies; it reads the others' too
 
             // S = K Q^T
             float sc[NT][2][4];
@@ -658,6 +659,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             // O = O + V^T P
             uint32_t vw[8][VW];
             each<8>([&](auto i) { take<D / 16, 4 * i * S::kRow>(from_v, vw[i]); });
+            __syncwarp();  // the last reads of this stage, which the next fetch() fills again
 #pragma unroll
             for (int j = 0; j < VW; ++j)
 #pragma unroll
