@@ -565,7 +565,9 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             take<4, S::kSteps + 4 * kTile>(slot_out + lane * 4, &steps[1]);
             const bool live = own >= max(begin, 1) && own < end && (valid >> (2 * (kStages<D, NT, BF16> - 1) + (lane >> 4)) & 1);
             const uint32_t vbits = live ? steps[1] & 0x7f800000u : 0u;
-            const bool bad = vbits == 0x7f800000u;  // a value step that is not finite: NaN for the rows that see it, and for no others
+            // a step that is not finite: NaN for the rows that see it, and for no others (an infinite key step would turn a
+            // negative product into the score that hides a position)
+            const bool bad = live && max(vbits, steps[0] & 0x7f800000u) == 0x7f800000u;
             const float kstep = bad ? CUDART_NAN_F : (live ? __uint_as_float(steps[0]) : 0.0f);
             const float vstep = live && !bad ? __uint_as_float(steps[1]) : 0.0f;
             const uint32_t live_bits = __ballot_sync(0xffffffffu, live);

@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         }
         if (warp < kPos / 32) {
             const uint32_t bits = __float_as_uint(vs) & 0x7f800000u;
-            const bool live = own != kNowhere, bad = live && bits == 0x7f800000u;  // NaN for the rows that see it, and for no others
+            // a step that is not finite: NaN for the rows that see it, and for no others (see kv4_rows_kernel)
+            const bool live = own != kNowhere, bad = live && max(bits, __float_as_uint(ks) & 0x7f800000u) == 0x7f800000u;
             k_steps[tid] = bad ? CUDART_NAN_F : ks;
             v_steps[tid] = bad ? 0.0f : vs;
             const uint32_t live_bits = __ballot_sync(0xffffffffu, live);

@@ -652,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 }
                 vexp = min(max(vexp, __reduce_max_sync(0xffffffffu, most)), 0x7e000000u);
                 const float own = (warp & 2) ? ((warp & 1) ? vs[3] : vs[2]) : ((warp & 1) ? vs[1] : vs[0]);
-                const bool bad = !(fabsf(own) < CUDART_INF_F);  // NaN for the rows that see it, and for no others
+                // a step that is not finite: NaN for the rows that see it, and for no others (see kv4_rows_kernel)
+                const bool bad = !(fabsf(own) < CUDART_INF_F && fabsf(ks) < CUDART_INF_F);
                 const int st = j % kStepStages, sk = j % kKS;
                 const uint32_t steps_at = base + S::kSteps + st * 1024, meta = base + S::kMeta + st * 32, kt = base + S::kK + sk * S::kTile;
                 if (j >= kKS && !mbar_wait_warp(k_empty + 8 * sk, (j / kKS - 1) & 1, p.status)) break;
