@@ -625,7 +625,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                             if (y[nt][i] != -CUDART_INF_F) most = fmaxf(most, sc[nt][i >> 2][i & 3] * (st[i >> 1] * factor[nt][c]));
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-                        most = fmaxf(most - kOff<BF16>, ref[nt][c]);
+                        // only the rows that ask for it, so that a row does not depend on its neighbours
+                        most = most - ref[nt][c] > kOff<BF16> + kLag<BF16> ? most - kOff<BF16> : ref[nt][c];
                         const float a = ex2(ref[nt][c] - most);
                         ref[nt][c] = most;
                         l[nt][c] *= a;
