@@ -486,7 +486,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                         if constexpr (!BF16)
                             qf[nt][NP - 1][j][m][e] = pack2(y0 - __half2float(__float2half_rn(y0)), y1 - __half2float(__float2half_rn(y1)));
                     }
-            const float f = p.scale * kLog2e * (1.0f / up);  // of row n in lanes 4 n ...
+            // of row n in lanes 4 n ...; an infinite query is NaN, as scores of one sign alone would hide every position
+            const float f = top < CUDART_INF_F ? p.scale * kLog2e * (1.0f / up) : CUDART_NAN_F;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 factor[nt][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));

@@ -368,9 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const uint32_t up_bits = min(max(0x86000000u - (top & 0x7f800000u), 0x07800000u), 0x7e800000u);
-                // a NaN: the row's other values do not matter
-                const float up = top > 0 && top <= 0x7f800000u ? __uint_as_float(up_bits) : 1.0f;
-                const float sup = p.scale < 0.0f ? -up : up;
+                // a row that is not finite is NaN everywhere, as infinite scores of one sign alone would hide every position
+                const float up = top > 0 && top < 0x7f800000u ? __uint_as_float(up_bits) : 1.0f;
+                const float sup = top < 0x7f800000u ? (p.scale < 0.0f ? -up : up) : CUDART_NAN_F;
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {

@@ -56,3 +56,44 @@ def test_a_written_key_with_an_infinite_value_is_not_lost(bits, dtype, new):
     sees = (torch.arange(300 - new, 300) >= 70).to(DEV)
     assert out[sees].isnan().all() and lse[sees].isnan().all()
     assert out[~sees].isfinite().all() and lse[~sees].isfinite().all()
+
+
+@pytest.mark.parametrize("new", [1, 30, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_an_infinite_query_makes_its_row_nan(dim, dtype, new):
+    # codes of one sign in the dimension where the query is infinite, so that all its scores are so too
+    m = 200
+    k, v = (rows_like_keys((m, 2, dim), s) for s in (1, 2))
+    k[:, 0, 7], k[:, 1, 7] = 4.0, -4.0
+    whole = Batch([m], [m], 32)
+    c = tb.KV4Cache.empty(whole.pages, 2, dim, page_size=32)
+    tb.bitnet_kv4_write(k.to(DEV), v.to(DEV), c, *whole.tensors(DEV))
+    batch = Batch([m], [new], 32)
+    good = queries(new, 4, dim, dtype)
+    for window in (0, 1, 50):
+        for causal in (True, False) if window == 0 else (True,):
+            want = run_attention(batch, c, good, causal=causal, window=window)
+            for bad in (INF, -INF, math.nan):
+                q = good.clone()
+                rows = sorted({0, new // 2, new - 1})
+                q[rows, 1, 7], q[rows, 2, 7] = bad, bad
+                got = run_attention(batch, c, q, causal=causal, window=window)
+                keep = torch.ones(q.shape[:2], dtype=torch.bool, device=DEV)
+                keep[rows, 1:3] = False
+                for g, w in zip(got, want):
+                    assert g[rows, 1:3].isnan().all(), (window, causal, bad)
+                    assert torch.equal(g[keep], w[keep])
+
+
+@pytest.mark.parametrize("new", [3, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_row_that_sees_nothing_is_zero_whatever_its_query(dim, dtype, new):
+    batch = Batch([new - 2], [new], 32)  # the first two rows stand before the cache
+    c, _ = filled(batch, 2, dim, 32)
+    q = queries(new, 4, dim, dtype)
+    q[0, :, 3], q[1, :, 5] = INF, math.nan
+    out, lse = run_attention(batch, c, q)
+    assert not out[:2].any() and (lse[:2] == -INF).all()
+    assert out[2:].isfinite().all() and lse[2:].isfinite().all()
