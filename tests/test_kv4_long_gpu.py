@@ -73,3 +73,31 @@ def test_references_and_units_that_move_late(heads, dtype, dim):
     q = queries(batch.rows, heads, dim, dtype)
     out, lse = run_attention(batch, c, q)
     check_heads(batch, c, q, out, lse, [heads - 1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("heads,m", [(56, 12000), (1, 30000)])  # whole, and cut into eight parts
+def test_fp32_sums_of_one_sign_are_not_cut(heads, m, dim):
+    """Values of one sign and nearly equal weights: roundings to nearest of such a sum's m terms lie on both sides and add
+    up to a few sqrt(m) / 2 of them, roundings that always cut add up to m.  Allowed: what check_attention allows without its
+    term for scores, which queries of 1e-3 leave at most 0.1 * 2^-24 each, so 2 sqrt(m) + 32 roundings (251 for 12,000); and
+    for the mean over all outputs, whose roundings to nearest have no common sign, one in eight of that."""
+    g = torch.Generator(DEV).manual_seed(dim)
+    batch = Batch([m], [m], 64)
+    k = torch.randn((m, heads, dim), generator=g, device=DEV)
+    v = torch.rand((m, heads, dim), generator=g, device=DEV) + 0.5
+    c = written(batch, heads, dim, 64, k, v)
+    kr, vr = tb.bitnet_kv4_read(c, *batch.tensors(DEV), m)
+    new = 256
+    batch = Batch([m], [new], 64)
+    q = queries(new, heads, dim, "fp32") * 1e-3
+    out, _ = run_attention(batch, c, q)
+    off = []
+    for h in range(0, heads, 11):
+        z = q[:, h].double() @ kr[:, h].double().T * dim ** -0.5
+        z.masked_fill_(torch.arange(m, device=DEV) > torch.arange(m - new, m, device=DEV)[:, None], -float("inf"))
+        want = torch.softmax(z, -1) @ vr[:, h].double()
+        off.append((out[:, h].double() - want) / want)
+    off = torch.stack(off) / U
+    most = 2 * m ** 0.5 + 32
+    assert off.abs().max() <= most and off.mean().abs() <= most / 8, (off.abs().max(), off.mean(), most)
