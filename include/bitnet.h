@@ -407,7 +407,7 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *   calls; fp32 calls split queries and probabilities into two fp16 parts); sums run in a fixed
  *   order, so equal calls give equal bits (other T, batch or tables may divide the sums
  *   in other ways).  scale must be finite.  A weight times its value's step is rounded to
- *   11 bits (fp32 calls: 22), but no finer than to 2^-28 (2^-38) of the row's largest weight.
+ *   11 bits (fp32 calls: 22), but no finer than to 2^-31 (2^-38) of the row's largest weight.
  *   A row that sees a step or a query that is not finite is NaN; other rows are not touched by it.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -39,12 +39,13 @@ constexpr int kJoinSplit = 2;   // CTAs that join an item, each some of its rows
 constexpr int kWholeTiles = 18;
 constexpr int kItemCost = 16;   // what beginning and ending an item takes, in tiles
 // Weights are held as 2^(s - m + kOff), and a score may pass the running maximum m by kLag before
-// that moves: with a step ratio below 2 they stay below 2^15.  fp32 calls leave less room above,
-// for a finer second part.
+// that moves: with a step ratio below 2 they stay below 2^15.  The more below, the more references move and the finer the
+// smallest weights are: with 2^3 and 11 for bf16 calls these lost three bits for 1 % of the time (64 sequences of 256 to 8192
+// positions 84.3 us instead of 84.9).  fp32 calls leave less room above, for a finer second part.
 template <bool BF16>
-constexpr float kOff = BF16 ? 3.0f : 13.0f;
+constexpr float kOff = BF16 ? 6.0f : 13.0f;
 template <bool BF16>
-constexpr float kLag = BF16 ? 11.0f : 1.0f;
+constexpr float kLag = BF16 ? 8.0f : 1.0f;
 constexpr float kNone = -3.0e38f;  // reference (m - kOff) of a row that has seen nothing yet
 constexpr int kTilesFrom = 128;  // rows of a sequence from which on kv4_prefill.cu or kv4_chunk.cu takes them
 constexpr float kLog2e = 1.4426950408889634f;
@@ -233,7 +234,7 @@ __device__ __forceinline__ int64_t weight(const RowsParams &p, const Seq &s) {
 //
 // Scores stand in units of log2.  The running maximum m of a row moves only when a score
 // passes it by more than kLag, so most tiles have no reduction and no rescaling; weights
-// 2^(s - m + kOff) stay below 2^15 and keep fp16's eleven bits down to 2^-17 of the maximum.
+// 2^(s - m + kOff) stay below 2^15 and keep fp16's eleven bits down to 2^-20 of the maximum.
 // Value steps are divided by a power of two that none so far is twice as large as, which is the unit of O; in
 // fp32 calls none of the tile, whose product it scales in fp32.
 // Queries are scaled by a power of two into [2^14, 2^15); bf16 queries are then exact in
@@ -509,7 +510,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float w = ref[nt][c] == kNone ? 0.0f : (bos_bad ? CUDART_NAN_F : (BF16 ? 0x1p3f : 0x1p13f));
+                const float w = ref[nt][c] == kNone ? 0.0f : (bos_bad ? CUDART_NAN_F : (BF16 ? 0x1p6f : 0x1p13f));
                 l[nt][c] = g == 0 ? w : 0.0f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) o[nt][i][c] = o[nt][i][2 + c] = w == 0.0f ? 0.0f : w * bos_step;

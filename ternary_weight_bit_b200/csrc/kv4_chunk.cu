@@ -31,9 +31,9 @@ constexpr int kRows = 128, kPos = 64, kThreads = 256;
 constexpr uint32_t kNowhere = 0xffffffffu;
 // as in kv4_attention.cu
 template <bool BF16>
-constexpr float kOff = BF16 ? 3.0f : 13.0f;
+constexpr float kOff = BF16 ? 6.0f : 13.0f;
 template <bool BF16>
-constexpr float kLag = BF16 ? 11.0f : 1.0f;
+constexpr float kLag = BF16 ? 8.0f : 1.0f;
 constexpr float kNone = -3.0e38f;
 constexpr int kSplits = 8;  // parts of an item at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;

@@ -56,7 +56,7 @@ constexpr int kSoftmaxRegs = D == 128 ? 184 : 192;
 template <int D>
 constexpr int kOtherRegs = 256 - kSoftmaxRegs<D>;
 constexpr uint32_t kNowhere = 0xffffffffu;
-constexpr float kOff = 3.0f, kLag = 11.0f, kNone = -3.0e38f;
+constexpr float kOff = 6.0f, kLag = 8.0f, kNone = -3.0e38f;
 constexpr int kSplits = 8;  // parts of an item at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
