@@ -407,7 +407,11 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *   calls; fp32 calls split queries and probabilities into two fp16 parts); sums run in a fixed
  *   order, so equal calls give equal bits (other T, batch or tables may divide the sums
  *   in other ways).  scale must be finite.  A weight times its value's step is rounded to
- *   11 bits (fp32 calls: 22), but no finer than to 2^-31 (2^-38) of the row's largest weight.
+ *   11 bits (fp32 calls: 22), but no finer than to 2^-31 (2^-38) of the row's largest weight times a value
+ *   step: the largest of 32 positions around it for sequences of fewer than 128 rows of a key head (new tokens x
+ *   q_heads / heads), of 64 for longer ones in fp32 calls, and in bf16 calls the largest up to the end of its 128
+ *   positions, those that the row does not see included.  Weights times values, weights up to 2^14, are summed
+ *   in fp32: values from about 2^113 / kv_lens[b] on can overflow.
  *   A row that sees a step or a query that is not finite is NaN; other rows are not touched by it.
  * ------------------------------------------------------------------------ */
 typedef struct {

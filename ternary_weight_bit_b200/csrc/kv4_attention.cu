@@ -235,8 +235,9 @@ __device__ __forceinline__ int64_t weight(const RowsParams &p, const Seq &s) {
 // Scores stand in units of log2.  The running maximum m of a row moves only when a score
 // passes it by more than kLag, so most tiles have no reduction and no rescaling; weights
 // 2^(s - m + kOff) stay below 2^15 and keep fp16's eleven bits down to 2^-20 of the maximum.
-// Value steps are divided by a power of two that none so far is twice as large as, which is the unit of O; in
-// fp32 calls none of the tile, whose product it scales in fp32.
+// A tile's value steps are divided by a power of two that none is twice as large as, which scales the
+// tile's product in fp32.  (With O in the products' own registers, in units of the largest step so far, two long sequences
+// took 1 % less; positions behind a far larger step lost their bits.)
 // Queries are scaled by a power of two into [2^14, 2^15); bf16 queries are then exact in
 // fp16 down to 2^-28 of the row's maximum.  fp32 calls carry queries and weights as the
 // sum of two fp16 numbers (22 bits).
@@ -500,12 +501,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         }
 
         float l[NT][2], o[NT][D / 16][4];
-        float bos_step = bos_page >= 0 ? p.c.v_step[kv4_rows(p.c, bos_page, kh)] : 0.0f;
+        const float bos_step = bos_page >= 0 ? p.c.v_step[kv4_rows(p.c, bos_page, kh)] : 0.0f;
         const bool bos_bad = !(fabsf(bos_step) < CUDART_INF_F);  // as for the other positions: NaN for the rows that see it
-        // bf16: O is in units of this power of two, which no value step so far is twice as large as
-        uint32_t units = max(bos_bad ? 0u : __float_as_uint(bos_step) & 0x7f800000u, 0x0d000000u);
-        units = min(units, 0x7e000000u);
-        if (BF16) bos_step *= __uint_as_float(0x7f000000u - units);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -573,17 +570,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             const float kstep = bad ? CUDART_NAN_F : (live ? __uint_as_float(steps[0]) : 0.0f);
             const float vstep = live && !bad ? __uint_as_float(steps[1]) : 0.0f;
             const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
-            const uint32_t vexp = min(max(__reduce_max_sync(0xffffffffu, bad ? 0u : vbits), BF16 ? units : 0x0d000000u), 0x7e000000u);
-            if (BF16 && vexp != units) {
-                const float f = __uint_as_float(units) * __uint_as_float(0x7f000000u - vexp);
-                units = vexp;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[nt][i][e] *= f;
-            }
+            const uint32_t vexp = min(max(__reduce_max_sync(0xffffffffu, bad ? 0u : vbits), 0x0d000000u), 0x7e000000u);
             const float vtop = __uint_as_float(vexp);
             const float vrel = vstep * __uint_as_float(0x7f000000u - vexp);
             const bool edge = at < all_begin || at + kTile > all_end || live_bits != 0xffffffffu;
@@ -680,27 +667,21 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
 #pragma unroll
                         for (int odd = 0; odd < 2; ++odd) {
                             float(&dst)[4] = o[nt][4 * j + 2 * u + odd];
-                            if constexpr (BF16) {
+                            // the tensor cores' sums are cut short: they end with the tile
+                            float acc[4];
 #pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    mma_f16(dst, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2], pf[nt][0][h][0], pf[nt][0][h][1]);
-                            } else {
-                                // the tensor cores' sums are cut short: they end with the tile
-                                float acc[4];
+                            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h)
+                                for (int k2 = NP - 1; k2 >= 0; --k2) {
+                                    if (h == 0 && k2 == NP - 1)
+                                        mma_f16_first(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2],
+                                                      pf[nt][k2][h][0], pf[nt][k2][h][1]);
+                                    else
+                                        mma_f16(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2], pf[nt][k2][h][0],
+                                                pf[nt][k2][h][1]);
+                                }
 #pragma unroll
-                                    for (int k2 = NP - 1; k2 >= 0; --k2) {
-                                        if (h == 0 && k2 == NP - 1)
-                                            mma_f16_first(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2],
-                                                          pf[nt][k2][h][0], pf[nt][k2][h][1]);
-                                        else
-                                            mma_f16(acc, x[h][0][odd], x[h][0][odd + 2], x[h][1][odd], x[h][1][odd + 2], pf[nt][k2][h][0],
-                                                    pf[nt][k2][h][1]);
-                                    }
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) dst[i] = fmaf(vtop, acc[i], dst[i]);
-                            }
+                            for (int i = 0; i < 4; ++i) dst[i] = fmaf(vtop, acc[i], dst[i]);
                         }
                 }
             advance(slot_out);
@@ -709,7 +690,6 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
         __syncthreads();  // every warp is done with its ring
 
         // join the warps
-        const float out_unit = BF16 ? __uint_as_float(units) : 1.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -721,8 +701,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int d = g * (D / 8) + 8 * (i >> 2) + 4 * ((i >> 1) & 1) + (i & 1);
-                    so[(warp * R + n) * LD + d] = o[nt][i][c] * out_unit;
-                    so[(warp * R + n) * LD + d + 2] = o[nt][i][2 + c] * out_unit;
+                    so[(warp * R + n) * LD + d] = o[nt][i][c];
+                    so[(warp * R + n) * LD + d + 2] = o[nt][i][2 + c];
                 }
             }
         __syncthreads();

@@ -48,3 +48,30 @@ def test_weights_far_below_the_largest(new, dim):
     err = err + 2.0 ** -31 * vv.abs().sum(0)[None]  # every step but that of the zero row is one and the same
     off = (got.cpu().double() - want).abs()
     assert (off <= err).all(), float((off / err).max())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 8])
+@pytest.mark.parametrize("m,size", [(500, 28), (570, 29), (3000, 28)])
+def test_a_large_value_step_touches_its_own_tile_alone(m, size, new, dim):
+    # Values 2^28 times the others' at positions whose weight is 0, one in each warp's first tile of 32 positions: few rows hold
+    # what follows them as finely as without them.  2^e is the power of two of the largest step of a tile.
+    g = torch.Generator().manual_seed(2)
+    sign = torch.where(torch.randn(dim, generator=g) > 0, 1.0, -1.0)
+    k, v = sign.expand(m, 1, dim).clone(), 1.0 + torch.rand((m, 1, dim), generator=g)
+    for pos in (5, 40, 70, 100):
+        k[pos], v[pos] = -sign, v[pos] * 2.0 ** size
+    c, (kv, vv), held = cache_of(k, v, 32)
+    gap = float((kv[7, 0] - kv[5, 0]) @ sign.double()) * dim ** -0.5
+    q = (sign * (60 * 0.6931471805599453 / gap)).expand(new, 8, dim).to(BF16).to(DEV)  # 2^-60 for the large
+    batch = Batch([m], [new], 32)
+    got, _ = run_attention(batch, c, q)
+    want, err = reference(q, kv, vv)
+    at, off = Batch([m], [m], 32).table[0].long()[torch.arange(m) // 32], torch.arange(m) % 32
+    step = held["v_step"][at, 0, off].double()
+    code = vv.abs()[:, 0] / step[:, None]
+    large = torch.cat([s.max().log2().floor().exp2().expand(s.numel()) for s in step.split(32)])
+    # m - 5 positions of the largest weight (position 0, at 8 bits, has less), so each is off by 2^-31 2^e |code| over their number
+    err = err + (2.0 ** -31 * large[:, None] * code).sum(0) / (m - 5)
+    d = (got.cpu().double() - want).abs()
+    assert (d <= err).all(), float((d / err).max())
