@@ -401,8 +401,8 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *            the choice of kernel; results stay right where it is wrong).  Worth giving where
  *            T counts many rows that belong to no sequence.
  *   ws       device scratch of at least bitnet_kv4_attention_workspace_bytes(...) bytes
- *            (256-byte aligned; BITNET_ERR_WORKSPACE if smaller).  Its contents need no
- *            initialisation.  Calls that may run at the same time need one each.
+ *            (256-byte aligned; BITNET_ERR_WORKSPACE if smaller), a size of the current device as the
+ *            call is.  Its contents need no initialisation.  Calls that may run at the same time need one each.
  *   Products and sums are fp32 (codes and scaled queries enter the tensor cores exactly in bf16
  *   calls; fp32 calls split queries and probabilities into two fp16 parts); sums run in a fixed
  *   order, so equal calls give equal bits (other T, batch or tables may divide the sums

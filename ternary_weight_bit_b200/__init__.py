@@ -564,9 +564,19 @@ def bitnet_kv4_read(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.T
 
 
 @functools.lru_cache(maxsize=4096)
-def bitnet_kv4_attention_workspace_bytes(T: int, q_heads: int, heads: int, dim: int, batch: int) -> int:
-    """Workspace of bitnet_kv4_attention for T rows of q_heads over a cache of `heads` key heads (0: sizes it refuses)."""
-    return _native.load().bitnet_kv4_attention_workspace_bytes(T, q_heads, heads, dim, batch)
+def _kv4_workspace_bytes(index: int, *sizes: int) -> int:
+    """The size on CUDA device `index` (it depends on the number of SMs), which is asked for with that device current."""
+    with torch.cuda.device(index):
+        return _native.load().bitnet_kv4_attention_workspace_bytes(*sizes)
+
+
+def bitnet_kv4_attention_workspace_bytes(T: int, q_heads: int, heads: int, dim: int, batch: int, device=None) -> int:
+    """Workspace of bitnet_kv4_attention for T rows of q_heads over a cache of `heads` key heads (0: sizes it refuses), on
+    `device` (the current one unless given)."""
+    if not torch.cuda.is_available():
+        return _native.load().bitnet_kv4_attention_workspace_bytes(T, q_heads, heads, dim, batch)
+    index = None if device is None else device if isinstance(device, int) else torch.device(device).index
+    return _kv4_workspace_bytes(torch.cuda.current_device() if index is None else index, T, q_heads, heads, dim, batch)
 
 
 def bitnet_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -593,7 +603,7 @@ def bitnet_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Te
         _need(lse, "lse", torch.float32, (T, heads))
     if ws is None:
         ws = _empty(cache.k_codes,
-                    (bitnet_kv4_attention_workspace_bytes(T, heads, cache.heads, cache.dim, batch.batch) or 256,), stream)
+                    (_kv4_workspace_bytes(dev.index, T, heads, cache.heads, cache.dim, batch.batch) or 256,), stream)
     else:
         _need(ws, "ws", torch.uint8)
     if out.device != dev or ws.device != dev or (lse is not None and lse.device != dev):
