@@ -278,7 +278,7 @@ kv4_read_kernel(Kv4Cache c, Kv4Batch bt, int64_t T, void *__restrict__ k_out, vo
     float step[kIter];
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-        w[it] = 0x88888888u, step[it] = 0.0f;
+        w[it] = 0u, step[it] = 0.0f;  // what is nowhere reads as 0 (of code 0: not -0)
         if (FEW && it > 0) {
             at = place[id.token(it)];
             first = kv4_rows(c, max(at.page, 0), id.first) + at.row;
