@@ -425,7 +425,8 @@ class KV4Cache:
     dim 64, 128 or 256).  The object keeps the tensors' addresses; a batch of sequences is described to the
     calls by three int32 CUDA tensors:
 
-        block_table [B, max_pages]  page of position s of sequence b: block_table[b, s // page_size]
+        block_table [B, max_pages]  page of position s of sequence b: block_table[b, s // page_size]; may be a part
+                                    of the columns of a wider table
         kv_lens     [B]             positions in the cache, this step's rows included
         q_starts    [B + 1]         sequence b owns rows q_starts[b]:q_starts[b + 1] of the token tensors, at
                                     its last positions
@@ -477,18 +478,22 @@ def _kv4_batch(cache: KV4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor
         good = (kv_lens.shape == (B,) and q_starts.shape == (B + 1,) and
                 block_table.dtype is torch.int32 and kv_lens.dtype is torch.int32 and q_starts.dtype is torch.int32 and
                 block_table.device == dev and kv_lens.device == dev and q_starts.device == dev and
-                block_table.is_contiguous() and kv_lens.is_contiguous() and q_starts.is_contiguous())
+                kv_lens.is_contiguous() and q_starts.is_contiguous())
+        stride, unit = block_table.stride()
+        good = good and (block_table.is_contiguous() or ((unit == 1 or width == 1) and (stride >= width or B == 1)))
     except (AttributeError, ValueError):
         good = False
     if not good:
         B = kv_lens.shape[0] if isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1 else -1
         _need(kv_lens, "kv_lens", torch.int32, (B,))
         _need(q_starts, "q_starts", torch.int32, (B + 1,))
-        _need(block_table, "block_table", torch.int32)
+        _need(block_table[:0] if isinstance(block_table, torch.Tensor) and block_table.dim() else block_table, "block_table", torch.int32)
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
+        if block_table.numel() and (block_table.stride(1) != 1 or block_table.stride(0) < block_table.shape[1]):
+            raise ValueError("block_table's rows must be contiguous and lie one behind the other")
         raise ValueError(f"block_table, kv_lens and q_starts must be on the cache's device {dev}")
-    return _native.Kv4Batch(block_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr(), width, B, width)
+    return _native.Kv4Batch(block_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr(), max(stride, width), B, width)
 
 
 def _rows(t: torch.Tensor, name: str, cache: KV4Cache, heads=None):
