@@ -36,6 +36,7 @@ template <bool BF16>
 constexpr float kLag = BF16 ? 8.0f : 1.0f;
 constexpr float kNone = -3.0e38f;
 constexpr int kSplits = 8;  // parts of an item at most
+constexpr float kKeyUnit = 0x1p-16f;  // as in kv4_prefill.cu
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct ChunkParams {
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             if constexpr (!BF16)
                 sts128(to + S::kQPart, rest2(x[0], x[4], h[0]), rest2(x[1], x[5], h[1]), rest2(x[2], x[6], h[2]), rest2(x[3], x[7], h[3]));
             // 1 / up, a power of two
-            const float f = fmaxf(fabsf(p.scale) * kLog2e * __uint_as_float(0x7f000000u - __float_as_uint(up)), 1.0e-37f);
+            const float f = fmaxf(fabsf(p.scale) * (kLog2e / kKeyUnit) * __uint_as_float(0x7f000000u - __float_as_uint(up)), 1.0e-37f);
 #pragma unroll
             for (int k = 0; k < 32 / L; ++k) {
                 const float y = __shfl_sync(0xffffffffu, f, k * L);
@@ -299,7 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     uint32_t vexp = 0x0d000000u;  // 2^-101: O is in units of this power of two, which no value step so far is twice as large as
     const uint32_t magic[2] = {p.magic[0], p.magic[1]};
-    const __half2 off = __float2half2_rn(-1032.0f), off16 = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
+    // of the low and the high nibbles of keys (in units of kKeyUnit) and of values
+    const __half2 one[2] = {__float2half2_rn(kKeyUnit), __float2half2_rn(1.0f)};
+    const __half2 off[2] = {__float2half2_rn(-1032.0f * kKeyUnit), __float2half2_rn(-1032.0f)};
+    const __half2 sixteenth[2] = {__float2half2_rn(0.0625f * kKeyUnit), __float2half2_rn(0.0625f)};
+    const __half2 off16[2] = {__float2half2_rn(-72.0f * kKeyUnit), __float2half2_rn(-72.0f)};
     float *const k_steps = reinterpret_cast<float *>(smem + S::kSteps), *const v_steps = k_steps + kPos;
     uint32_t *const meta = reinterpret_cast<uint32_t *>(smem + S::kMeta);
     // what a lane's part of a tile of 8 x 8 loads is at: rows lane % 8 (+ 8), pieces 0 or 1
@@ -322,10 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
                 const uint32_t w = *reinterpret_cast<const uint32_t *>(smem + S::kCodes + side * (kPos * D / 2) + x * 4), v = w >> 8;
-                sts128(to + side * (S::kV - S::kK), h2(__hadd2(as_h2((w & 0x000F000Fu) ^ magic[0]), off)),
-                       h2(__hfma2(as_h2((w & 0x00F000F0u) ^ magic[1]), sixteenth, off16)),
-                       h2(__hadd2(as_h2((v & 0x000F000Fu) ^ magic[0]), off)),
-                       h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth, off16)));
+                sts128(to + side * (S::kV - S::kK), h2(__hfma2(as_h2((w & 0x000F000Fu) ^ magic[0]), one[side], off[side])),
+                       h2(__hfma2(as_h2((w & 0x00F000F0u) ^ magic[1]), sixteenth[side], off16[side])),
+                       h2(__hfma2(as_h2((v & 0x000F000Fu) ^ magic[0]), one[side], off[side])),
+                       h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth[side], off16[side])));
             }
         }
         if (at0 == 0) {  // position 0 is kept at 8 bits
@@ -335,7 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
                 const int side = tid / (D / 8), c = tid % (D / 8);
                 const char4 *const c8 = reinterpret_cast<const char4 *>((side ? p.c.v_bos : p.c.k_bos) + (int64_t)(r >> p.c.page_log2) * D + 8 * c);
                 const char4 a = c8[0], e = c8[1];
-                sts128(base + S::kK + side * (S::kV - S::kK) + (c << 4), pack2(a.x, e.x), pack2(a.y, e.y), pack2(a.z, e.z), pack2(a.w, e.w));
+                const float u = side ? 1.0f : kKeyUnit;
+                sts128(base + S::kK + side * (S::kV - S::kK) + (c << 4), pack2(a.x * u, e.x * u), pack2(a.y * u, e.y * u),
+                       pack2(a.z * u, e.z * u), pack2(a.w * u, e.w * u));
             }
         }
         if (warp < kPos / 32) {

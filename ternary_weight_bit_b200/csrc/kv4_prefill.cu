@@ -39,6 +39,8 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 namespace bitnet {
 
 namespace {
@@ -58,6 +60,9 @@ constexpr int kOtherRegs = 256 - kSoftmaxRegs<D>;
 constexpr uint32_t kNowhere = 0xffffffffu;
 constexpr float kOff = 6.0f, kLag = 8.0f, kNone = -3.0e38f;
 constexpr int kSplits = 8;  // parts of an item at most
+// Key codes stand in this unit (exactly: fp16 has multiples of 2^-24), which the rows' factors undo: products with queries of up to
+// 2^15 stay below 2^14, so that with their key's step they pass fp32's range only where that is over 2^114.
+constexpr float kKeyUnit = 0x1p-16f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // n / d for 0 <= n < 2^31 by a multiplication: with 2^l >= d, m = floor(2^32 (2^l - d) / d) + 1.
@@ -216,14 +221,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 
 // Eight codes of a word as 16 bytes of fp16, dimensions in the order 0 4 1 5 2 6 3 7 (see halves() in
-// kv4_attention.cu).
+// kv4_attention.cu), times kKeyUnit for keys.
+template <bool KEYS>
 __device__ __forceinline__ void put_codes(uint32_t dst, uint32_t w, const uint32_t (&magic)[2]) {
+    constexpr float kUnit = KEYS ? kKeyUnit : 1.0f;
     const uint32_t v = w >> 8;
-    const __half2 off = __float2half2_rn(-1032.0f), off16 = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
-    sts128(dst, h2(__hadd2(as_h2((w & 0x000F000Fu) ^ magic[0]), off)),
-           h2(__hfma2(as_h2((w & 0x00F000F0u) ^ magic[1]), sixteenth, off16)),
-           h2(__hadd2(as_h2((v & 0x000F000Fu) ^ magic[0]), off)),
-           h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth, off16)));
+    const __half2 one = __float2half2_rn(kUnit), off = __float2half2_rn(-1032.0f * kUnit);
+    const __half2 sixteenth = __float2half2_rn(0.0625f * kUnit), off16 = __float2half2_rn(-72.0f * kUnit);
+    auto low = [&](uint32_t x) { return KEYS ? __hfma2(as_h2(x), one, off) : __hadd2(as_h2(x), off); };
+    sts128(dst, h2(low((w & 0x000F000Fu) ^ magic[0])), h2(__hfma2(as_h2((w & 0x00F000F0u) ^ magic[1]), sixteenth, off16)),
+           h2(low((v & 0x000F000Fu) ^ magic[0])), h2(__hfma2(as_h2((v & 0x00F000F0u) ^ magic[1]), sixteenth, off16)));
 }
 
 template <int D>
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 sts128(at(rr), pack2(y[0], y[4]), pack2(y[1], y[5]), pack2(y[2], y[6]), pack2(y[3], y[7]));
                 if (piece == 0)  // 1 / up, a power of two
                     sts32(base + S::kFactors + 4 * (w * kRows + rr),
-                          __float_as_uint(fmaxf(fabsf(p.scale) * kLog2e * __uint_as_float(0x7f000000u - __float_as_uint(up)), 1.0e-37f)));
+                          __float_as_uint(fmaxf(fabsf(p.scale) * (kLog2e / kKeyUnit) * __uint_as_float(0x7f000000u - __float_as_uint(up)), 1.0e-37f)));
             }
             fence_proxy_async_smem();
             arrive(q_full);
@@ -571,18 +578,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
         const uint32_t magic[2] = {p.magic[0], p.magic[1]};
-        auto put_piece = [&](uint32_t tile, int i, int q, const uint4 &c) {  // 32 dimensions of position i
+        auto put_piece = [&](auto keys, uint32_t tile, int i, int q, const uint4 &c) {  // 32 dimensions of position i
             const uint32_t x[4] = {c.x, c.y, c.z, c.w};
             const uint32_t row = tile + (q >> 1) * (kRows * 128) + i * 128;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) put_codes(row + ((((4 * q + e) & 7) ^ (i & 7)) << 4), x[e], magic);
+            for (int e = 0; e < 4; ++e) put_codes<decltype(keys)::value>(row + ((((4 * q + e) & 7) ^ (i & 7)) << 4), x[e], magic);
         };
-        auto put_bos = [&](uint32_t tile, int q, const int8_t *c8) {  // 32 dimensions of position 0, kept at 8 bits
+        auto put_bos = [&](auto keys, uint32_t tile, int q, const int8_t *c8) {  // 32 dimensions of position 0, kept at 8 bits
+            constexpr float u = decltype(keys)::value ? kKeyUnit : 1.0f;
 #pragma unroll 1
             for (int e = 0; e < 4; ++e) {
                 const char4 a = *reinterpret_cast<const char4 *>(c8 + 32 * q + 8 * e), c = *reinterpret_cast<const char4 *>(c8 + 32 * q + 8 * e + 4);
-                sts128(tile + (q >> 1) * (kRows * 128) + (((4 * q + e) & 7) << 4), pack2(a.x, c.x), pack2(a.y, c.y), pack2(a.z, c.z),
-                       pack2(a.w, c.w));
+                sts128(tile + (q >> 1) * (kRows * 128) + (((4 * q + e) & 7) << 4), pack2(a.x * u, c.x * u), pack2(a.y * u, c.y * u),
+                       pack2(a.z * u, c.z * u), pack2(a.w * u, c.w * u));
             }
         };
         if (warp < 12) {
@@ -663,9 +671,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 if (i == 0) sts32(meta + 16, vexp);
                 arrive(st_full + 8 * st);
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) put_piece(kt, i, q, kc[q]);
+                for (int q = 0; q < D / 32; ++q) put_piece(std::true_type(), kt, i, q, kc[q]);
                 if (live && (step0 + j) * kPos + i == 0)
-                    for (int q = 0; q < D / 32; ++q) put_bos(kt, q, p.c.k_bos + (int64_t)(r >> p.c.page_log2) * D);
+                    for (int q = 0; q < D / 32; ++q) put_bos(std::true_type(), kt, q, p.c.k_bos + (int64_t)(r >> p.c.page_log2) * D);
                 fence_proxy_async_smem();
                 arrive(k_full + 8 * sk);
                 if (j + 1 < steps) ok = load(j + 1, next);
@@ -697,11 +705,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < kRounds; ++k) {
                     const int x = v + k * kValueThreads;
-                    if (x < kPieces) put_piece(vt, x / (D / 32), x % (D / 32), c[k]);
+                    if (x < kPieces) put_piece(std::false_type(), vt, x / (D / 32), x % (D / 32), c[k]);
                 }
                 if (step0 + j == 0 && v < D / 32) {
                     const uint32_t r = lds32(base + S::kPlaces + (j % kPlaceStages) * 512);
-                    if (r != kNowhere) put_bos(vt, v, p.c.v_bos + (int64_t)(r >> p.c.page_log2) * D);
+                    if (r != kNowhere) put_bos(std::false_type(), vt, v, p.c.v_bos + (int64_t)(r >> p.c.page_log2) * D);
                 }
                 fence_proxy_async_smem();
                 arrive(v_full + 8 * sv);

@@ -1,0 +1,29 @@
+"""Keys and queries of very different sizes whose products are ordinary numbers: no intermediate passes fp32's range where the
+scores do not, and few and many rows agree."""
+import pytest
+import torch
+
+import kv4_ref
+import ternary_weight_bit_b200 as tb
+from kv4_ref import Batch
+from test_kv4_gpu import DEV, DTYPES, _clean_status, check_attention, copies, queries, rows_like_keys, rubbish_cache, run_attention  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("new", [1, 30, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("size", [1e-30, 1e-20, 1e20, 1e28, 1e33])
+def test_large_keys_and_small_queries(size, dim, dtype, new):
+    m = 260
+    batch = Batch([m], [m], 64)
+    c = rubbish_cache(batch.pages, 2, dim, 64)
+    k, v = rows_like_keys((m, 2, dim), 21) * size, rows_like_keys((m, 2, dim), 22)
+    tb.bitnet_kv4_write(k.to(DEV), v.to(DEV), c, *batch.tensors(DEV), eps=1e-5 if size > 1 else 1e-36)
+    held = copies(c)
+    held = [tuple(kv4_ref.values(held[s + "_codes"], held[s + "_step"], held[s + "_bos"], batch, 0) for s in "kv")]
+    q = (queries(new, 4, dim, "fp32") * (1 / size)).to(DTYPES[dtype])
+    batch = Batch([m], [new], 64)
+    out, lse = run_attention(batch, c, q)
+    check_attention(batch, c, held, q, out, lse, dim ** -0.5, True, 0)
