@@ -473,7 +473,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 z0 *= p.scale * kLog2e * p.c.k_step[kv4_rows(p.c, bos_page, kh)];
             }
             // up = 2^(14 - exponent), kept inside the normal numbers (a row below 2^-112 is then scaled less)
-            const uint32_t up_bits = min(max(0x86000000u - (__float_as_uint(top) & 0x7f800000u), 0x07800000u), 0x7e800000u);
+            const uint32_t up_bits = min(max(0x86000000u - (__float_as_uint(top) & 0x7f800000u), 0x07000000u), 0x7e800000u);
             const float up = top > 0.0f ? __uint_as_float(up_bits) : 1.0f;
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) x[i] *= up;

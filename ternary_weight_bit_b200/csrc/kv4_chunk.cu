@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const uint32_t up_bits = min(max(0x86000000u - (top & 0x7f800000u), 0x07800000u), 0x7e800000u);
+            const uint32_t up_bits = min(max(0x86000000u - (top & 0x7f800000u), 0x07000000u), 0x7e800000u);
             // a row that is not finite is NaN everywhere, as infinite scores of one sign alone would hide every position
             const float up = top > 0 && top < 0x7f800000u ? __uint_as_float(up_bits) : 1.0f;
             const float sup = top < 0x7f800000u ? (p.scale < 0.0f ? -up : up) : CUDART_NAN_F;

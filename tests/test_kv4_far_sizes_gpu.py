@@ -27,3 +27,24 @@ def test_large_keys_and_small_queries(size, dim, dtype, new):
     batch = Batch([m], [new], 64)
     out, lse = run_attention(batch, c, q)
     check_attention(batch, c, held, q, out, lse, dim ** -0.5, True, 0)
+
+
+@pytest.mark.parametrize("new", [200])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_queries_up_to_the_largest_number(dim, dtype, new):
+    m = 260
+    batch = Batch([m], [m], 64)
+    c = rubbish_cache(batch.pages, 2, dim, 64)
+    k, v = rows_like_keys((m, 2, dim), 23) * 1e-36, rows_like_keys((m, 2, dim), 24)
+    tb.bitnet_kv4_write(k.to(DEV), v.to(DEV), c, *batch.tensors(DEV), eps=1e-38)
+    held = copies(c)
+    held = [tuple(kv4_ref.values(held[s + "_codes"], held[s + "_step"], held[s + "_bos"], batch, 0) for s in "kv")]
+    q = queries(new, 4, dim, "fp32")
+    q = q / q.abs().amax(-1, keepdim=True) * 3e36
+    q = q.to(DTYPES[dtype])
+    q[:, 1::2, 5] = torch.finfo(q.dtype).max
+    q[:, 3, 9] = -torch.finfo(q.dtype).max
+    batch = Batch([m], [new], 64)
+    out, lse = run_attention(batch, c, q)
+    check_attention(batch, c, held, q, out, lse, dim ** -0.5, True, 0)
