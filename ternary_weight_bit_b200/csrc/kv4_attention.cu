@@ -459,6 +459,13 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // up = 2^(14 - exponent), kept inside the normal numbers (a row below 2^-112 is then scaled less)
+            const uint32_t up_bits = min(max(0x86000000u - (__float_as_uint(top) & 0x7f800000u), 0x07000000u), 0x7e800000u);
+            const float up = top > 0.0f ? __uint_as_float(up_bits) : 1.0f;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) x[i] *= up;
+            // of row n in lanes 4 n ...; an infinite query is NaN, as scores of one sign alone would hide every position
+            const float f = top < CUDART_INF_F ? p.scale * kLog2e * (1.0f / up) : CUDART_NAN_F;
             float z0 = 0.0f;  // this row's product with position 0
             if (bos_page >= 0) {
                 const int8_t *c8 = p.c.k_bos + ((int64_t)bos_page * p.c.heads + kh) * D + t * (D / 4);
@@ -470,13 +477,8 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 }
                 z0 += __shfl_xor_sync(0xffffffffu, z0, 1);
                 z0 += __shfl_xor_sync(0xffffffffu, z0, 2);
-                z0 *= p.scale * kLog2e * p.c.k_step[kv4_rows(p.c, bos_page, kh)];
+                z0 *= f * p.c.k_step[kv4_rows(p.c, bos_page, kh)];
             }
-            // up = 2^(14 - exponent), kept inside the normal numbers (a row below 2^-112 is then scaled less)
-            const uint32_t up_bits = min(max(0x86000000u - (__float_as_uint(top) & 0x7f800000u), 0x07000000u), 0x7e800000u);
-            const float up = top > 0.0f ? __uint_as_float(up_bits) : 1.0f;
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) x[i] *= up;
 #pragma unroll
             for (int j = 0; j < KW; ++j)
 #pragma unroll
@@ -488,8 +490,6 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                         if constexpr (!BF16)
                             qf[nt][NP - 1][j][m][e] = pack2(y0 - __half2float(__float2half_rn(y0)), y1 - __half2float(__float2half_rn(y1)));
                     }
-            // of row n in lanes 4 n ...; an infinite query is NaN, as scores of one sign alone would hide every position
-            const float f = top < CUDART_INF_F ? p.scale * kLog2e * (1.0f / up) : CUDART_NAN_F;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 factor[nt][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));

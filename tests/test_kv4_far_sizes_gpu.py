@@ -29,7 +29,7 @@ def test_large_keys_and_small_queries(size, dim, dtype, new):
     check_attention(batch, c, held, q, out, lse, dim ** -0.5, True, 0)
 
 
-@pytest.mark.parametrize("new", [200])
+@pytest.mark.parametrize("new", [1, 30, 200])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_queries_up_to_the_largest_number(dim, dtype, new):
