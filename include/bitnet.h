@@ -402,7 +402,8 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *            T counts many rows that belong to no sequence.
  *   ws       device scratch of at least bitnet_kv4_attention_workspace_bytes(...) bytes
  *            (256-byte aligned; BITNET_ERR_WORKSPACE if smaller), a size of the current device as the
- *            call is.  Its contents need no initialisation.  Calls that may run at the same time need one each.
+ *            call is, and of the call's own sizes: a smaller T can need more, as few rows are divided among
+ *            more CTAs.  Its contents need no initialisation.  Calls that may run at the same time need one each.
  *   Products and sums are fp32 (codes and scaled queries enter the tensor cores exactly in bf16
  *   calls; fp32 calls split queries and probabilities into two fp16 parts); sums run in a fixed
  *   order, so equal calls give equal bits (other T, batch or tables may divide the sums
@@ -410,8 +411,7 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *   11 bits (fp32 calls: 22), but no finer than to 2^-31 (2^-38) of the row's largest weight times a value
  *   step: the largest of 32 positions around it for sequences of fewer than 128 rows of a key head (new tokens x
  *   q_heads / heads), of 64 for longer ones in fp32 calls, and in bf16 calls the largest up to the end of its 128
- *   positions, those that the row does not see included.  Weights times values, weights up to 2^14, are summed
- *   in fp32: values from about 2^113 / kv_lens[b] on can overflow.
+ *   positions, those that the row does not see included.
  *   A row that sees a step or a query that is not finite is NaN; other rows are not touched by it.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -577,7 +577,7 @@ def _kv4_workspace_bytes(index: int, *sizes: int) -> int:
 
 def bitnet_kv4_attention_workspace_bytes(T: int, q_heads: int, heads: int, dim: int, batch: int, device=None) -> int:
     """Workspace of bitnet_kv4_attention for T rows of q_heads over a cache of `heads` key heads (0: sizes it refuses), on
-    `device` (the current one unless given)."""
+    `device` (the current one unless given).  A smaller T can need more, as few rows are divided among more CTAs."""
     if not torch.cuda.is_available():
         return _native.load().bitnet_kv4_attention_workspace_bytes(T, q_heads, heads, dim, batch)
     index = None if device is None else device if isinstance(device, int) else torch.device(device).index

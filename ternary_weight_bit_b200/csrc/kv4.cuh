@@ -6,6 +6,10 @@
 
 namespace bitnet {
 
+// Weights are held up to 2^14; sums of weights times values stand over that, so that they pass fp32's range
+// no sooner than with weights up to 1.
+constexpr float kSumUnit = 0x1p14f;
+
 // Records a status (the first one stays) in the device status word.
 __device__ __forceinline__ void record_status(int *status, int code) {
     if (status) atomicCAS(status, 0, code);

@@ -510,7 +510,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
                 const float w = ref[nt][c] == kNone ? 0.0f : (bos_bad ? CUDART_NAN_F : (BF16 ? 0x1p6f : 0x1p13f));
                 l[nt][c] = g == 0 ? w : 0.0f;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) o[nt][i][c] = o[nt][i][2 + c] = w == 0.0f ? 0.0f : w * bos_step;
+                for (int i = 0; i < D / 16; ++i) o[nt][i][c] = o[nt][i][2 + c] = w == 0.0f ? 0.0f : w / kSumUnit * bos_step;
             }
         if (bos_page >= 0) {
             const int8_t *c8 = p.c.v_bos + ((int64_t)bos_page * p.c.heads + kh) * D + g * (D / 8);
@@ -571,7 +571,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             const float vstep = live && !bad ? __uint_as_float(steps[1]) : 0.0f;
             const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
             const uint32_t vexp = min(max(__reduce_max_sync(0xffffffffu, bad ? 0u : vbits), 0x0d000000u), 0x7e000000u);
-            const float vtop = __uint_as_float(vexp);
+            const float vtop = __uint_as_float(vexp) / kSumUnit;
             const float vrel = vstep * __uint_as_float(0x7f000000u - vexp);
             const bool edge = at < all_begin || at + kTile > all_end || live_bits != 0xffffffffu;
 
@@ -727,7 +727,7 @@ kv4_rows_kernel(const __grid_constant__ RowsParams p) {
             }
             const int r = row0 + n, tok = r / p.group;
             const int64_t at = (int64_t)(q0 + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = sum == 0.0f ? 0.0f : kSumUnit / sum;
             if constexpr (BF16)
                 *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.out) + at * D + d) = make_uint2(
                     h2_bf16(y.x * inv, y.y * inv), h2_bf16(y.z * inv, y.w * inv));
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
         const int r = h.y + n, tok = r / p.group;
         if ((int64_t)h.x + tok >= p.T) continue;
         const int64_t at = ((int64_t)h.x + tok) * p.q_heads + kh * p.group + (r - tok * p.group);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = sum == 0.0f ? 0.0f : kSumUnit / sum;
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
             const int64_t d = at * D + V * lane + e;

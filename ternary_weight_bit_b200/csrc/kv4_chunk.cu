@@ -495,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             float *const dst = p.part + ((int64_t)item * p.splits + part) * (D + 2) * kRows + rr;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
-                dst[(8 * i + t) * kRows] = o[i][2 * c] * unit;
-                dst[(8 * i + t + 4) * kRows] = o[i][2 * c + 1] * unit;
+                dst[(8 * i + t) * kRows] = o[i][2 * c] * (unit / kSumUnit);
+                dst[(8 * i + t + 4) * kRows] = o[i][2 * c + 1] * (unit / kSumUnit);
             }
             if (t == 0) {
                 dst[D * kRows] = ref[c];
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_consta
     for (int s = 0; s < kSplits; ++s) top = fmaxf(top, w[s]);
 #pragma unroll
     for (int s = 0; s < kSplits; ++s) w[s] = ex2(w[s] - top), sum = fmaf(w[s], l[s], sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : kSumUnit / sum;
     if (warp == 0) {
         places[lane] = place;
         if (p.lse && place >= 0) p.lse[place] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;

@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const __grid_con
                 constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};  // dimension of a group's column
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    dst[(32 * c + (i & ~7) + order[i & 7]) * (2 * kRows)] = steps > 0 && ok ? __uint_as_float(o[i]) * __uint_as_float(vexp) : 0.0f;
+                    dst[(32 * c + (i & ~7) + order[i & 7]) * (2 * kRows)] = steps > 0 && ok ? __uint_as_float(o[i]) * (__uint_as_float(vexp) / kSumUnit) : 0.0f;
             }
             dst[D * (2 * kRows)] = ok ? ref : kNone;
             dst[(D + 1) * (2 * kRows)] = ok ? l : 0.0f;
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(256) kv4_tiles_join_kernel(const __grid_consta
     for (int s = 0; s < kSplits; ++s) top = fmaxf(top, w[s]);
 #pragma unroll
     for (int s = 0; s < kSplits; ++s) w[s] = ex2(w[s] - top), sum = fmaf(w[s], l[s], sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : kSumUnit / sum;
     if (warp == 0) {
         places[lane] = place;
         if (p.lse && place >= 0) p.lse[place] = sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;

@@ -48,3 +48,22 @@ def test_queries_up_to_the_largest_number(dim, dtype, new):
     batch = Batch([m], [new], 64)
     out, lse = run_attention(batch, c, q)
     check_attention(batch, c, held, q, out, lse, dim ** -0.5, True, 0)
+
+
+@pytest.mark.parametrize("new,length", [(1, 500), (1, 9000), (30, 500), (200, 260), (200, 9000)])  # whole and in parts
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("bits", [3, 4])
+def test_values_near_the_largest_number(bits, dim, dtype, new, length):
+    # sums of weights times values stay in range where the values' own sum over all positions does
+    batch = Batch([length], [length], 64)
+    c = rubbish_cache(batch.pages, 1, dim, 64)
+    k, v = rows_like_keys((length, 1, dim), 25), rows_like_keys((length, 1, dim), 26)
+    v = v / v.abs().sum() * dim * 3e38
+    tb.bitnet_kv4_write(k.to(DEV), v.to(DEV), c, *batch.tensors(DEV), bits=bits)
+    held = copies(c)
+    held = [tuple(kv4_ref.values(held[s + "_codes"], held[s + "_step"], held[s + "_bos"], batch, 0) for s in "kv")]
+    q = queries(new, 4, dim, dtype)
+    batch = Batch([length], [new], 64)
+    out, lse = run_attention(batch, c, q)
+    check_attention(batch, c, held, q, out, lse, dim ** -0.5, True, 0)
