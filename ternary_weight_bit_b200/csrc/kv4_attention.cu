@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ R
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int share = ((h.z & 255) + kJoinSplit - 1) / kJoinSplit, first = blockIdx.y * share;
     const int nrows = min(share, (h.z & 255) - first), kh = h.z >> 8;
-    if (nrows <= 0 || nrows > R || (unsigned)kh >= (unsigned)p.c.heads || h.x < 0 || h.y < 0) return;
+    if (nrows <= 0 || nrows > R || (unsigned)kh >= (unsigned)p.c.heads || h.x < 0 || (unsigned)h.y > (unsigned)INT32_MAX - R) return;
     const int log2 = nrows > 4 ? 0 : (nrows > 2 ? 1 : (nrows > 1 ? 2 : 3));  // warps of a row
     for (int n0 = 0; n0 < nrows; n0 += W >> log2) {
         const int n = first + n0 + (warp >> log2);
