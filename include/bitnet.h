@@ -376,7 +376,8 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *     s = 0:            stat = max|x|,  Q = 127,    codes in [-128, 127]  (k_bos / v_bos)
  *     s >= 1, bits = 4: stat = mean|x|, Q = sqrt 7, codes in [-8, 7]
  *     s >= 1, bits = 3: stat = max|x|,  Q = 3,      codes in [-4, 3]
- *     code = clamp(rne(x * (Q / (stat + eps)))),  step = (stat + eps) / Q.
+ *     code = clamp(rne(x * (Q / (stat + eps)))),  step = (stat + eps) / Q, which is formed in fp32: up to 15
+ *     roundings of 2^-24 (rows that went through fp64 have one).
  *   k, v     [T][heads][dim] fp32 or bf16 (dt); element (t, h, d) of either at
  *            t * token_stride + h * head_stride + d (elements; row starts must be 16-byte aligned).
  *   Rows whose position would be negative (n_b > kv_lens[b]) are skipped.
@@ -411,7 +412,9 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *   11 bits (fp32 calls: 22), but no finer than to 2^-31 (2^-38) of the row's largest weight times a value
  *   step: the largest of 32 positions around it for sequences of fewer than 128 rows of a key head (new tokens x
  *   q_heads / heads), of 64 for longer ones in fp32 calls, and in bf16 calls the largest up to the end of its 128
- *   positions, those that the row does not see included.
+ *   positions, those that the row does not see included.  The tensor cores cut where they add: fp32 calls and
+ *   sequences of fewer than 128 rows end their sums of at most 64 positions in fp32, longer ones in bf16 calls do not, and
+ *   outputs of values of one sign come out low there by about 3e-9 to a position (half a step of bf16 is 2e-3 to 4e-3).
  *   A row that sees a step or a query that is not finite is NaN; other rows are not touched by it.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -10,9 +10,9 @@
 // padded for groups of up to 8.
 //
 // What bounds it: 64 sequences of 256 to 8192 positions, 32 query heads on 8 of dim 128, one new
-// token each (296 MB of cache): 84 us, 3.5 TB/s; two of 131072 and 111869 positions with 64 query heads:
-// 70 us, 3.8 TB/s.  The same kernel without its arithmetic takes 70 and 53 us: a tile costs a warp 620 instructions
-// (300 of them turn nibbles into fp16 and 32 are products), which keeps 60 % of the issue slots and half of the
+// token each (296 MB of cache): 85 us, 3.5 TB/s; two of 131072 and 111869 positions with 64 query heads:
+// 71 us, 3.7 TB/s.  Without its arithmetic the kernel took 70 and 53 us of 84 and 70: a tile costs a warp 620 instructions
+// (300 of them turn nibbles into fp16 and 32 are products), which keeps 61 % of the issue slots and half of the
 // integer units busy, and an item's beginning and end take as long as 16 tiles of its CTA.  fp32 calls double
 // the products: 4 sequences of 4096 positions, 32 heads each with its own keys, 34 us.  Tried, and no
 // faster: bulk copies (107 us where these took 99), four CTAs to an SM, codes as subnormal fp16 (2 % at the cost

@@ -13,11 +13,11 @@
 // twice.  Each group of 8 dimensions stands in the order 0 4 1 5 2 6 3 7, as the nibbles come out of a
 // word; queries are stored in the same order and outputs are put back.
 //
-// What bounds it: a prompt of 2048 tokens, 32 query heads on 8, takes 228 us in fp32 at dim 128 (two products to
-// each of the formula's: 301 TFLOP/s of them) and 297 in bf16 at dim 256 (231 TFLOP/s), against 550 and 943 of
-// kv4_rows_kernel.  The tensor cores' mma.sync path is busy for 54 and 42 % of the time; unpacking
+// What bounds it: a prompt of 2048 tokens, 32 query heads on 8, takes 247 us in fp32 at dim 128 (two products to
+// each of the formula's: 278 TFLOP/s of them) and 316 in bf16 at dim 256 (217 TFLOP/s), against 550 and 943 of
+// kv4_rows_kernel.  The tensor cores' mma.sync path is busy for 50 and 39 % of the time; unpacking
 // and the two barriers of a step are not covered by products, as one CTA fills an SM's registers.  Tried, and no
-// faster: two steps' tiles with one barrier a step (232 and 314), products in groups of four sums.
+// faster: two steps' tiles with one barrier a step (1 and 5 % slower), products in groups of four sums.
 #include "kv4.cuh"
 
 #include <cuda_fp16.h>
@@ -457,8 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         }
         if constexpr (!BF16) {
             // The tensor cores cut where they add, so their sums end with the step: kept over 12,000 positions of one sign they
-            // were low by 144 * 2^-24 of the output, over 30,000 by 450, and are by 2 so (for 2 to 4 % of the time).  For
-            // bf16 outputs, of which half a step is 32,768 * 2^-24, O stays in the products' own registers.
+            // were low by 144 * 2^-24 of the output, over 30,000 by 450, and are by 2 so (for 2 to 4 % of the time).  In bf16
+            // calls, where it would be 8 to 10 %, O stays in the products' own registers: values of one sign over 30,000 positions
+            // are low by 1240 * 2^-24, where half a step of the output is 32,768 to 65,536.
             const float to_o = __uint_as_float(own_vexp) * __uint_as_float(0x7f000000u - vexp);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {

@@ -22,16 +22,21 @@
 // stands in shared memory in the order 0 4 1 5 2 6 3 7, as the nibbles come out of a word; queries
 // are stored in the same order and outputs are put back.
 //
+// O stays in the tensor memory through all positions of an item's part.  The tensor cores cut where they add, so values of one
+// sign come out low by about 3e-9 to a position: 1500 * 2^-24 over 30,000, where half a step of a bf16 output is 32,768 to
+// 65,536.  (Sums that end with a step would move O through registers in each.)
+//
 // As in kv4_attention.cu, a row's reference moves only when a score passes it by more than kLag,
 // and value steps are divided by a power of two that no step so far is twice as large as; O is
 // rescaled in TMEM in those rare cases alone.
 //
 // What bounds it: a step (both tiles, 128 positions) takes 5700 cycles at dim 128 and 4400 at dim 64, of which
 // the exponentials hold their unit for 2048 and the products the tensor cores for 1700; the rest is the chain
-// product - load - maximum - exponentials - store - product of each tile, which the other tile's covers in part.  S
-// and O fill the tensor memory, so that no third tile fits at dim 128.  Beginning and ending an item takes 6 to 10 us
-// more.  Prompts of 4100, 1999 and 3298 tokens, 32 query heads on 8 of dim 128: 423 us, 614 TFLOP/s.  1024 and 637
-// tokens at the ends of 16500 and 13719 at dim 64: 456 us, 447 TFLOP/s.  Tried, and no faster: S in two halves of 64
+// product - load - maximum - exponentials - store - product of each tile, which the other tile's covers in part.  (S and
+// O of two tiles fill the tensor memory at dim 128.  Within a tile, the product with V could begin before the last
+// exponential, and S be loaded again instead of held in registers: not tried.)  Beginning and ending an item takes 6 to 10 us
+// more.  Prompts of 4100, 1999 and 3298 tokens, 32 query heads on 8 of dim 128: 427 us, 608 TFLOP/s.  1024 and 637
+// tokens at the ends of 16500 and 13719 at dim 64: 458 us, 446 TFLOP/s.  Tried, and no faster: S in two halves of 64
 // positions in turns, 16 warps of softmax, exponentials by a polynomial on the fp32 units, weights in columns
 // of their own at dim 64.
 #include "kv4.cuh"
