@@ -369,6 +369,8 @@ BITNET_API bitnet_status_t bitnet_kv_quant(const void *kv, bitnet_dtype_t xdt, i
  *   position is then not written, reads as zeros, and is not attended.  Sequences of a
  *   batch may share pages for reading; rows written by one call must lie in different
  *   places.
+ *   batch is at most 32768, T at most 2^30 in every call, table_stride at least max_pages, and strides of token
+ *   tensors at most 2^32 elements (BITNET_ERR_INVALID_ARG otherwise).
  *
  * bitnet_kv4_write: quantises new rows and writes them to their positions.
  *   Row x of position s, in real arithmetic (decided in fp64 wherever fp32 is near a border,
